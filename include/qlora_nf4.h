@@ -29,8 +29,10 @@
  *
  * Beyond the single layer: several adapters sharing X packed into one layer
  * (qlora_grouped_*), the layer without a saved X A^T (XA_saved = NULL: recomputed), the
- * SwiGLU glue (flat or on a packed gate/up output) and the LM head + cross-entropy over a
- * frozen NF4 head, chunked over tokens (qlora_lm_head_ce).
+ * SwiGLU glue (flat or on a packed gate/up output), the residual update with its RMS norms
+ * (qlora_residual_norm_*), rotary positions on the packed q/k/v output (qlora_rope), AdamW over
+ * the adapters (qlora_adamw_step) and the LM head + cross-entropy over a frozen NF4 head, chunked
+ * over tokens (qlora_lm_head_ce).
  *
  * Conventions for every entry point:
  *   - Pointers named as device memory are caller-owned device allocations on the current
@@ -63,7 +65,8 @@ typedef enum {
   QLORA_OK = 0,
   QLORA_ERR_NULL = 1,      /* a required pointer is NULL */
   QLORA_ERR_SHAPE = 2,     /* M < 1, N or K not a multiple of 64, r out of range: [1, 128] for
-                              qlora_linear_*, multiples of 8 in [8, 128] for the other calls */
+                              qlora_linear_*, multiples of 8 in [8, 128] for the other calls;
+                              any other argument outside the range its call documents */
   QLORA_ERR_ALIGN = 3,     /* a device pointer is not 16-byte aligned */
   QLORA_ERR_ARCH = 4,      /* current device is not compute capability 10.0 (sm_100a) */
   QLORA_ERR_WORKSPACE = 5, /* workspace NULL or smaller than qlora_workspace_bytes() */
@@ -217,6 +220,159 @@ QLORA_API qlora_status qlora_swiglu_packed_fwd(const void* gu, void* a, int64_t 
                                                qlora_stream_t stream);
 QLORA_API qlora_status qlora_swiglu_packed_bwd(const void* gu, const void* da, void* dgu,
                                                int64_t M, int I, qlora_stream_t stream);
+
+/* ---- Residual update of a block with its RMS norms. ----
+ * Per token row ("Unsloth vs QLoRA vs Liger-Kernel", section 2: RMSNorm among the
+ * hand-differentiated ops; the norm after the block, its gate and the scales are the usual
+ * extensions of it):
+ *   a  = y r_y (w_post + o),   r_y = 1 / sqrt(mean(y^2) + eps)      (a = y when w_post is NULL)
+ *   h' = res_scale h + branch_scale gate a                          (stored in h's type)
+ *   n  = h' r_h (w_pre + o),   r_h = 1 / sqrt(mean(h'^2) + eps)     (of h' as stored)
+ * o = weight_offset (1 for weights kept as their difference from one).  y NULL: no update, n is
+ * the norm of h (h_out, w_post, gate and rstd_post must then be NULL, gate_kind none).  w_pre
+ * NULL: no n (rstd_pre and n NULL).  At least one of y and w_pre is given.
+ * Types: y and n bf16; h and h_out fp32 with QLORA_F32_RESIDUAL in `types`, else bf16; w_pre
+ * and w_post fp32 with QLORA_F32_WEIGHTS; the gate fp32 with QLORA_F32_GATE.  The gate is NULL,
+ * [D], [M] or [M, D] by gate_kind.  rstd_pre, rstd_post [M] fp32 are kept for the backward (NULL:
+ * not kept).  fp32 arithmetic, one rounding at each output.  1 <= D <= 16384, M >= 0 (M = 0 does
+ * nothing).  h_out may be h, n may be y. */
+enum { QLORA_F32_RESIDUAL = 1, QLORA_F32_WEIGHTS = 2, QLORA_F32_GATE = 4 };
+enum { QLORA_GATE_NONE = 0, QLORA_GATE_CHANNEL = 1, QLORA_GATE_TOKEN = 2, QLORA_GATE_FULL = 3 };
+QLORA_API qlora_status qlora_residual_norm_fwd(const void* h, const void* y, const void* w_pre,
+                                               const void* w_post, const void* gate,
+                                               int gate_kind, int64_t M, int D, int types,
+                                               float eps, float res_scale, float branch_scale,
+                                               float weight_offset, void* h_out, void* n,
+                                               float* rstd_pre, float* rstd_post,
+                                               qlora_stream_t stream);
+
+/* Its backward: gradients of h, y, the weights and the gate from dn (bf16, with w_pre) and dh_out
+ * (h's type, what later blocks send back along the residual; NULL: zero).  With x = h' r_h,
+ * z = y r_y, u = dn (w_pre + o):
+ *   G = dh_out + r_h (u - x mean(u x));  dh = res_scale G;           dw_pre  = sum_m dn x
+ *   E = branch_scale G;  dgate = E a, summed over what the gate is broadcast along;  E := gate E
+ *   t = E (w_post + o);  dy = r_y (t - z mean(t z));                 dw_post = sum_m E z
+ * (dy = E without w_post.)  h_out is the forward's output (h itself when it had no y).  y is read
+ * only for w_post or dgate and may be NULL otherwise; dy NULL: the forward had no branch.  dw_pre,
+ * dw_post [D] fp32 and dgate (fp32 [D], fp32 [M], or [M, D] in the gate's type) may be NULL:
+ * not computed.  dh may be dh_out, dy may be y or dn, for the same types.
+ * ws: scratch for the column sums of dw_pre, dw_post and a channel gate's dgate, at least
+ * qlora_residual_norm_workspace_bytes(M, D) bytes (may be NULL without those).  The sums are added
+ * in a fixed order. */
+QLORA_API size_t qlora_residual_norm_workspace_bytes(int64_t M, int D);
+QLORA_API qlora_status qlora_residual_norm_bwd(const void* dn, const void* dh_out,
+                                               const void* h_out, const void* y,
+                                               const float* rstd_pre, const float* rstd_post,
+                                               const void* w_pre, const void* w_post,
+                                               const void* gate, int gate_kind, int64_t M, int D,
+                                               int types, float res_scale, float branch_scale,
+                                               float weight_offset, void* dh, void* dy,
+                                               float* dw_pre, float* dw_post, void* dgate,
+                                               void* ws, size_t ws_bytes, qlora_stream_t stream);
+
+/* ---- Rotary positions on heads of queries and keys. ----
+ * ("Unsloth vs QLoRA vs Liger-Kernel", section 2: RoPE among the hand-differentiated ops.)  Pair i
+ * of a head, i < rotary_dim / 2, turns by position x f_i:
+ *   (a, b) -> scale (a cos - b sin, b cos + a sin),
+ * the pair being elements (i, i + rotary_dim / 2), or (2i, 2i + 1) with `interleaved`.  Elements
+ * from rotary_dim on pass through.  `inverse` turns the other way: the backward pass, applied to
+ * the gradients.
+ *
+ * Host-only: phase[i] = f_i / (2 pi) x 2^64, rounded, of rotary_dim / 2 pairs (copied to the
+ * device by the caller), and *scale.  f_i = base^(-2i / rotary_dim), then by `kind`:
+ *   QLORA_ROPE_PLAIN    as it is;
+ *   QLORA_ROPE_LINEAR   f / factor;
+ *   QLORA_ROPE_BASE     base x factor^(rd / (rd - 2)) in place of base (rd > 2): the slowest pair is
+ *                       slowed by factor, the fastest not at all;
+ *   QLORA_ROPE_BANDS    with b = clamp((original f / 2 pi - low) / (high - low), 0, 1):
+ *                       f (b + (1 - b) / factor);
+ *   QLORA_ROPE_RAMP     with d(n) = rd ln(original / (2 pi n)) / (2 ln base), from
+ *                       l = max(floor d(high), 0) to e = min(ceil d(low), rd - 1) the blend
+ *                       s = clamp((i - l) / max(e - l, 0.001), 0, 1):
+ *                       f (1 - s + s / factor), and *scale = 0.1 ln(factor) + 1
+ * (*scale = 1 for the other kinds).  `low` < `high` are turns over the original length: pairs that
+ * turn less than low are slowed by factor, those above high kept.
+ * 2 <= rotary_dim <= 2048 and even, base > 1, factor >= 1, 0 < low, original > 0, all finite; the
+ * arguments that a kind does not name are not looked at. */
+enum { QLORA_ROPE_PLAIN = 0, QLORA_ROPE_LINEAR = 1, QLORA_ROPE_BASE = 2, QLORA_ROPE_BANDS = 3,
+       QLORA_ROPE_RAMP = 4 };
+QLORA_API qlora_status qlora_rope_phase(int rotary_dim, double base, int kind, double factor,
+                                        double low, double high, double original, uint64_t* phase,
+                                        float* scale);
+
+/* One tensor of heads: element i of head h of token (b, s) lies at b batch + s token + h head + i,
+ * in elements.  out may be x with the same strides (in place: elements from rotary_dim on are then
+ * not touched); otherwise the two must not overlap, and every head is written whole. */
+typedef struct {
+  const void* x;
+  void* out;
+  int64_t x_batch, x_token, x_head;
+  int64_t out_batch, out_token, out_head;
+  int heads;
+} qlora_rope_heads;
+
+/* Turns the heads of one or two tensors (q, and k or NULL) of B x S tokens, bf16 or (f32) fp32.
+ * positions: device [B S] int32, or int64 with pos64, of any sign and size; NULL: start + s.  The
+ * angle is exact at any position (a 64-bit fraction of a turn).  Pointers and strides only need
+ * the elements' alignment; 16-byte ones are faster.  rotary_dim <= head_dim <= 2048; at most
+ * 4096 heads in all.  B or S = 0 does nothing. */
+QLORA_API qlora_status qlora_rope(const qlora_rope_heads* q, const qlora_rope_heads* k, int64_t B,
+                                  int64_t S, int head_dim, int rotary_dim, int f32,
+                                  const void* positions, int pos64, int64_t start,
+                                  const uint64_t* phase, float scale, int interleaved,
+                                  int inverse, qlora_stream_t stream);
+
+/* ---- AdamW over many tensors at once: the step after qlora_linear_bwd's dA and dB. ----
+ * ("FTDD-03" teaching script: optimizer states in few bits.)  For every element of every tensor:
+ *   g = grad_scale clip grad;  m = b1 m + (1 - b1) g;  v = b2 v + (1 - b2) g^2
+ *   p = p (1 - lr wd) - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps),  t: this step, from 1
+ * with lr the tensor's lr x lr_scale and wd its weight_decay.  max_norm > 0:
+ * clip = min(1, max_norm / (norm + 1e-6)), norm = ||grad_scale grad|| over all tensors; with
+ * max_norm > 0 or check_finite the norm is computed first, and where it is not finite the call
+ * changes nothing but the state's norm and its count of skipped steps.
+ *   p       bf16, or fp32 with param_f32; read and written.  master: an fp32 copy that the step is
+ *           taken on (p is its bf16 rounding), or NULL: a bf16 p is then rounded stochastically.
+ *   grad    bf16, or fp32 with grad_f32.
+ * Elements are numbered in blocks of 256 over the list, every tensor starting a block: tensor i's
+ * element j is number 256 x (blocks of the tensors before) + j.  Moments are flat over that
+ * numbering (qlora_adamw_blocks() blocks), zero before the first step:
+ *   bits 32: m, v fp32; the scales are NULL.
+ *   bits 8:  one byte each, with one fp32 scale a block, its largest |m| or sqrt(v).  m: bit 7 the
+ *            sign, c = bits 0-6 the magnitude 2^(e - 127) (1 + f / 8), 8 e + f = 889 + c (c = 0: 0);
+ *            v: sqrt(v) = 2^(e - 127) (1 + f / 16), 16 e + f = 1777 + c (c = 0: 0), times the scale.
+ *            Codes are rounded stochastically with a hash of (seed, t, element's number); a v above
+ *            0 never becomes 0.  A gradient that is not finite makes its whole block not finite.
+ * state: 64 device bytes, zero before the first step: the count of steps taken is its first int64,
+ * the last norm the float at byte 8, the count of skipped steps the int32 at byte 16.
+ * lr_device: device float that takes the place of lr, or NULL.  ws: device scratch of
+ * qlora_adamw_workspace_bytes() bytes, needed with max_norm or check_finite.  A state and its ws
+ * belong to one sequence of calls.  n = 0 tensors are allowed; p, grad and master 16-byte aligned.
+ * Captured into a graph, a replay takes the next step. */
+typedef struct {
+  void* p;
+  float* master;
+  const void* grad;
+  int64_t n;
+  float lr_scale, weight_decay;
+  int param_f32, grad_f32;
+} qlora_adamw_tensor;
+typedef struct {
+  double lr, beta1, beta2, eps, grad_scale, max_norm;
+  const float* lr_device;
+  uint32_t seed;
+  int bits, check_finite;
+} qlora_adamw_config;
+/* Blocks of 256 elements of a list of tensors (host array); 0 for an invalid list. */
+QLORA_API int64_t qlora_adamw_blocks(const qlora_adamw_tensor* tensors, int count);
+QLORA_API size_t qlora_adamw_workspace_bytes(int count);
+QLORA_API qlora_status qlora_adamw_step(const qlora_adamw_tensor* tensors, int count,
+                                        const qlora_adamw_config* config, void* m, void* v,
+                                        float* m_scale, float* v_scale, void* state, void* ws,
+                                        size_t ws_bytes, qlora_stream_t stream);
+/* The values that `blocks` blocks of 8-bit moments stand for, as bf16 or (out_f32) fp32. */
+QLORA_API qlora_status qlora_adamw_moments(const void* m, const void* v, const float* m_scale,
+                                           const float* v_scale, int64_t blocks, int out_f32,
+                                           void* m_out, void* v_out, qlora_stream_t stream);
 
 /* ---- LM head + cross-entropy over a frozen NF4 head, chunked over tokens. ----
  * "Unsloth vs QLoRA vs Liger-Kernel", section 3 (fused cross-entropy): the projection to the

@@ -35,6 +35,15 @@ EXPORTS = (
     "qlora_grouped_bwd",
     "qlora_swiglu_packed_fwd",
     "qlora_swiglu_packed_bwd",
+    "qlora_residual_norm_fwd",
+    "qlora_residual_norm_workspace_bytes",
+    "qlora_residual_norm_bwd",
+    "qlora_rope_phase",
+    "qlora_rope",
+    "qlora_adamw_blocks",
+    "qlora_adamw_workspace_bytes",
+    "qlora_adamw_step",
+    "qlora_adamw_moments",
     "qlora_lm_head_ce_workspace_bytes",
     "qlora_lm_head_ce",
     "qlora_cross_entropy_count",
@@ -52,6 +61,11 @@ STATUS = {
     0: "QLORA_OK", 1: "QLORA_ERR_NULL", 2: "QLORA_ERR_SHAPE", 3: "QLORA_ERR_ALIGN",
     4: "QLORA_ERR_ARCH", 5: "QLORA_ERR_WORKSPACE", 6: "QLORA_ERR_CUDA", 7: "QLORA_ERR_TIMEOUT",
 }
+
+
+# `types` and `gate_kind` of the residual norm.
+F32_RESIDUAL, F32_WEIGHTS, F32_GATE = 1, 2, 4
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
 
 
 class QLoraError(RuntimeError):
@@ -73,10 +87,56 @@ class Nf4Weight(ctypes.Structure):
     ]
 
 
+class RopeHeads(ctypes.Structure):
+    """Mirror of ``qlora_rope_heads``."""
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("x_batch", ctypes.c_int64),
+        ("x_token", ctypes.c_int64),
+        ("x_head", ctypes.c_int64),
+        ("out_batch", ctypes.c_int64),
+        ("out_token", ctypes.c_int64),
+        ("out_head", ctypes.c_int64),
+        ("heads", ctypes.c_int),
+    ]
+
+
+class AdamWTensor(ctypes.Structure):
+    """Mirror of ``qlora_adamw_tensor``."""
+    _fields_ = [
+        ("p", ctypes.c_void_p),
+        ("master", ctypes.c_void_p),
+        ("grad", ctypes.c_void_p),
+        ("n", ctypes.c_int64),
+        ("lr_scale", ctypes.c_float),
+        ("weight_decay", ctypes.c_float),
+        ("param_f32", ctypes.c_int),
+        ("grad_f32", ctypes.c_int),
+    ]
+
+
+class AdamWConfig(ctypes.Structure):
+    """Mirror of ``qlora_adamw_config``."""
+    _fields_ = [
+        ("lr", ctypes.c_double),
+        ("beta1", ctypes.c_double),
+        ("beta2", ctypes.c_double),
+        ("eps", ctypes.c_double),
+        ("grad_scale", ctypes.c_double),
+        ("max_norm", ctypes.c_double),
+        ("lr_device", ctypes.c_void_p),
+        ("seed", ctypes.c_uint32),
+        ("bits", ctypes.c_int),
+        ("check_finite", ctypes.c_int),
+    ]
+
+
 _LIB = None
 _VP = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
+_D = ctypes.c_double
 _SZ = ctypes.c_size_t
 _I64 = ctypes.c_int64
 
@@ -115,6 +175,21 @@ def _lib():
             "qlora_grouped_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
             "qlora_swiglu_packed_fwd": (_I, [_VP, _VP, _I64, _I, _VP]),
             "qlora_swiglu_packed_bwd": (_I, [_VP, _VP, _VP, _I64, _I, _VP]),
+            "qlora_residual_norm_fwd": (_I, [_VP, _VP, _VP, _VP, _VP, _I, _I64, _I, _I, _F, _F,
+                                             _F, _F, _VP, _VP, _VP, _VP, _VP]),
+            "qlora_residual_norm_workspace_bytes": (_SZ, [_I64, _I]),
+            "qlora_residual_norm_bwd": (_I, [_VP] * 9 + [_I, _I64, _I, _I, _F, _F, _F]
+                                        + [_VP] * 6 + [_SZ, _VP]),
+            "qlora_rope_phase": (_I, [_I, _D, _I, _D, _D, _D, _D, ctypes.POINTER(_I64),
+                                      ctypes.POINTER(_F)]),
+            "qlora_rope": (_I, [ctypes.POINTER(RopeHeads), ctypes.POINTER(RopeHeads), _I64, _I64,
+                                _I, _I, _I, _VP, _I, _I64, _VP, _F, _I, _I, _VP]),
+            "qlora_adamw_blocks": (_I64, [ctypes.POINTER(AdamWTensor), _I]),
+            "qlora_adamw_workspace_bytes": (_SZ, [_I]),
+            "qlora_adamw_step": (_I, [ctypes.POINTER(AdamWTensor), _I,
+                                      ctypes.POINTER(AdamWConfig), _VP, _VP, _VP, _VP, _VP, _VP,
+                                      _SZ, _VP]),
+            "qlora_adamw_moments": (_I, [_VP, _VP, _VP, _VP, _I64, _I, _VP, _VP, _VP]),
             "qlora_lm_head_ce_workspace_bytes": (_SZ, [_I, _I, _I, _I]),
             "qlora_lm_head_ce": (_I, [_VP, ctypes.POINTER(Nf4Weight), _VP, _I, _I, _VP, _VP, _VP,
                                       _VP, _SZ, _VP]),
@@ -226,6 +301,68 @@ def qlora_swiglu_packed_fwd(gu, a, M, I, stream):
 
 def qlora_swiglu_packed_bwd(gu, da, dgu, M, I, stream):
     _check("qlora_swiglu_packed_bwd", _lib().qlora_swiglu_packed_bwd(gu, da, dgu, M, I, stream))
+
+
+def qlora_residual_norm_fwd(h, y, w_pre, w_post, gate, gate_kind, M, D, types, eps, res_scale,
+                            branch_scale, weight_offset, h_out, n, rstd_pre, rstd_post, stream):
+    _check("qlora_residual_norm_fwd",
+           _lib().qlora_residual_norm_fwd(h, y, w_pre, w_post, gate, gate_kind, M, D, types, eps,
+                                          res_scale, branch_scale, weight_offset, h_out, n,
+                                          rstd_pre, rstd_post, stream))
+
+
+def qlora_residual_norm_workspace_bytes(M, D):
+    return int(_lib().qlora_residual_norm_workspace_bytes(M, D))
+
+
+def qlora_residual_norm_bwd(dn, dh_out, h_out, y, rstd_pre, rstd_post, w_pre, w_post, gate,
+                            gate_kind, M, D, types, res_scale, branch_scale, weight_offset, dh, dy,
+                            dw_pre, dw_post, dgate, ws, ws_bytes, stream):
+    _check("qlora_residual_norm_bwd",
+           _lib().qlora_residual_norm_bwd(dn, dh_out, h_out, y, rstd_pre, rstd_post, w_pre, w_post,
+                                          gate, gate_kind, M, D, types, res_scale, branch_scale,
+                                          weight_offset, dh, dy, dw_pre, dw_post, dgate, ws,
+                                          ws_bytes, stream))
+
+
+def qlora_rope_phase(rotary_dim, base, kind, factor, low, high, original):
+    """(phases as a ctypes int64 array of rotary_dim / 2, scale)."""
+    phase = (_I64 * max(int(rotary_dim) // 2, 1))()
+    scale = _F()
+    _check("qlora_rope_phase",
+           _lib().qlora_rope_phase(int(rotary_dim), float(base), int(kind), float(factor),
+                                   float(low), float(high), float(original), phase,
+                                   ctypes.byref(scale)))
+    return phase, scale.value
+
+
+def qlora_rope(q, k, B, S, head_dim, rotary_dim, f32, positions, pos64, start, phase, scale,
+               interleaved, inverse, stream):
+    """q, k: RopeHeads (k or None)."""
+    _check("qlora_rope",
+           _lib().qlora_rope(q, k, B, S, head_dim, rotary_dim, f32, positions, pos64, start, phase,
+                             scale, interleaved, inverse, stream))
+
+
+def qlora_adamw_blocks(tensors, count):
+    return int(_lib().qlora_adamw_blocks(tensors, count))
+
+
+def qlora_adamw_workspace_bytes(count):
+    return int(_lib().qlora_adamw_workspace_bytes(count))
+
+
+def qlora_adamw_step(tensors, count, config, m, v, m_scale, v_scale, state, ws, ws_bytes, stream):
+    """tensors: an array of AdamWTensor; config: AdamWConfig."""
+    _check("qlora_adamw_step",
+           _lib().qlora_adamw_step(tensors, count, config, m, v, m_scale, v_scale, state, ws,
+                                   ws_bytes, stream))
+
+
+def qlora_adamw_moments(m, v, m_scale, v_scale, blocks, out_f32, m_out, v_out, stream):
+    _check("qlora_adamw_moments",
+           _lib().qlora_adamw_moments(m, v, m_scale, v_scale, blocks, int(out_f32), m_out, v_out,
+                                      stream))
 
 
 def qlora_lm_head_ce_workspace_bytes(M, V, K, chunk):

@@ -370,4 +370,123 @@ cudaError_t launch_swiglu_packed_fwd(const __nv_bfloat16* gu, __nv_bfloat16* a, 
 cudaError_t launch_swiglu_packed_bwd(const __nv_bfloat16* gu, const __nv_bfloat16* da,
                                      __nv_bfloat16* dgu, int64_t M, int I, cudaStream_t stream);
 
+// ------------------------------ residual update with its norms ------------------------------
+enum GateKind { kGateNone = 0, kGateChannel = 1, kGateToken = 2, kGateFull = 3 };
+constexpr int kNormMaxD = 16384;  // 1024 threads of 16 elements
+struct ResidualNormFwd {
+  const void* h;           // [M, D] fp32 when resid_f32, else bf16
+  const __nv_bfloat16* y;  // [M, D] or null: h goes to the norm as it is
+  const void* w_pre;       // [D] or null: no n
+  const void* w_post;      // [D] or null: y itself
+  const void* gate;        // by gate_kind: null, [D], [M] or [M, D]
+  void* h_out;             // as h (with y)
+  __nv_bfloat16* n;
+  float* rstd_pre;         // [M] or null
+  float* rstd_post;
+  int64_t M;
+  int D;
+  int gate_kind;
+  bool resid_f32, weight_f32, gate_f32;
+  float eps, res_scale, branch_scale, weight_offset;
+};
+struct ResidualNormBwd {
+  const __nv_bfloat16* dn;  // with w_pre
+  const void* dh_out;       // as h, or null: zero
+  const void* h_out;
+  const __nv_bfloat16* y;   // null where neither w_post nor dgate needs it
+  const float* rstd_pre;
+  const float* rstd_post;
+  const void* w_pre;
+  const void* w_post;
+  const void* gate;
+  void* dh;
+  __nv_bfloat16* dy;  // null: no branch
+  float* dw_pre;      // [D] or null
+  float* dw_post;
+  void* dgate;        // fp32 [D], fp32 [M] or as the gate [M, D]; or null
+  float* part;        // workspace: rows of column sums
+  int64_t M;
+  int D;
+  int part_ld;        // set by the launcher
+  int gate_kind;
+  bool resid_f32, weight_f32, gate_f32;
+  float res_scale, branch_scale, weight_offset;
+};
+cudaError_t launch_residual_norm_fwd(const ResidualNormFwd& a, cudaStream_t stream);
+// Workspace for the column sums of the weight and channel-gate gradients.
+size_t residual_norm_part_bytes(int64_t M, int D);
+// *launches: kernels launched.
+cudaError_t launch_residual_norm_bwd(const ResidualNormBwd& a, cudaStream_t stream, int* launches);
+
+// ------------------------------ rotary positions --------------------------------------------
+// One tensor of heads: element (b, s, head, i) at b batch + s token + head head + i (elements).
+struct RopeHeads {
+  const void* x;
+  void* out;
+  int64_t x_batch, x_token, x_head;
+  int64_t out_batch, out_token, out_head;
+  int heads;
+};
+struct RopeArgs {
+  RopeHeads t[2];          // the second has 0 heads where there is one tensor
+  const uint64_t* phase;   // [rotary_dim / 2] turns per position, times 2^64
+  const void* positions;   // [M] int32 or int64, or null: start + s
+  int64_t start;
+  int64_t M, S;            // tokens, tokens of one batch
+  int head_dim, rotary_dim;
+  bool f32, pos64, interleaved, inverse, copy;  // copy: out of place, the rest of each head too
+  float scale;
+};
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream);
+
+// ------------------------------ AdamW over many tensors -------------------------------------
+// Blocks of 256 elements are numbered through the list of tensors, each tensor starting one.
+constexpr int kAdamBlock = 256;
+constexpr int kAdamTensors = 512;  // tensors of one launch: 24 KB of kernel parameters
+struct AdamTensor {
+  void* p;            // bf16, or fp32 when param_f32
+  float* master;      // fp32 copy or null
+  const void* g;      // bf16, or fp32 when grad_f32
+  int64_t n;
+  uint32_t block0;    // first block of the tensor within the launch
+  uint32_t flags;     // 1: p fp32, 2: g fp32
+  float lr_scale, weight_decay;
+};
+struct AdamTable {
+  AdamTensor t[kAdamTensors];
+};
+struct AdamArgs {
+  int tensors;
+  uint32_t blocks;       // of this launch
+  int64_t first_block;   // of this launch within the list
+  void* m;               // fp32 or 8-bit codes, 256 a block over the list
+  void* v;
+  float* m_scale;        // one a block (8 bits)
+  float* v_scale;
+  void* state;           // AdamState
+  double* part;          // workspace: sums of squares, one a CTA
+  int part_first;        // this launch's first
+  int part_count;        // of the whole list
+  const float* lr_dev;   // or null: lr
+  float lr, b1, b2, one_b1, one_b2, eps, grad_scale, max_norm;
+  double b1d, b2d;
+  uint32_t seed;
+  bool bits8, use_norm, last;  // last: the launch that closes the step
+};
+struct AdamState {       // device, zero (or the steps taken so far) before the first step
+  int64_t step;          // steps taken
+  float norm;            // of the last step's gradients, scaled
+  float factor;          // on the gradients of the last step
+  int32_t skipped;       // steps left out for a norm that was not finite
+  uint32_t ticket;       // zero between launches
+  int32_t finite;
+  int32_t pad[9];
+};
+constexpr int kAdamNormCtas = 148 * 8;  // at most: one double of workspace each
+int adam_norm_ctas(uint32_t blocks);
+cudaError_t launch_adam_norm(const AdamTable& table, const AdamArgs& a, cudaStream_t stream);
+cudaError_t launch_adam_step(const AdamTable& table, const AdamArgs& a, cudaStream_t stream);
+cudaError_t launch_adam_moments(const AdamArgs& a, int64_t blocks, void* m_out, void* v_out,
+                                bool out_f32, cudaStream_t stream);
+
 }  // namespace qlora

@@ -1294,6 +1294,367 @@ qlora_status qlora_swiglu_packed_bwd(const void* gu, const void* da, void* dgu, 
   return st;
 }
 
+static bool finite_f(double x) { return std::isfinite(x); }
+
+qlora_status qlora_residual_norm_fwd(const void* h, const void* y, const void* w_pre,
+                                     const void* w_post, const void* gate, int gate_kind,
+                                     int64_t M, int D, int types, float eps, float res_scale,
+                                     float branch_scale, float weight_offset, void* h_out, void* n,
+                                     float* rstd_pre, float* rstd_post, qlora_stream_t stream) {
+  if (!h || (!y && !w_pre) || (w_pre && !n) || (y && !h_out)) return QLORA_ERR_NULL;
+  if (gate_kind != QLORA_GATE_NONE && !gate) return QLORA_ERR_NULL;
+  if (M < 0 || D < 1 || D > kNormMaxD || gate_kind < QLORA_GATE_NONE ||
+      gate_kind > QLORA_GATE_FULL || (types & ~7))
+    return QLORA_ERR_SHAPE;
+  // What nothing would write or read is a mistake of the caller's.
+  if (!y && (h_out || w_post || rstd_post || gate_kind != QLORA_GATE_NONE))
+    return QLORA_ERR_SHAPE;
+  if ((!w_pre && (n || rstd_pre)) || (!w_post && rstd_post) ||
+      (gate_kind == QLORA_GATE_NONE && gate))
+    return QLORA_ERR_SHAPE;
+  for (const void* p : {h, y, w_pre, w_post, gate, static_cast<const void*>(h_out),
+                        static_cast<const void*>(n), static_cast<const void*>(rstd_pre),
+                        static_cast<const void*>(rstd_post)})
+    if (!aligned16(p)) return QLORA_ERR_ALIGN;
+  if (M == 0) return QLORA_OK;
+  int dev;
+  qlora_status st = current_device(&dev);
+  if (st != QLORA_OK) return st;
+  ResidualNormFwd a = {};
+  a.h = h;
+  a.y = static_cast<const __nv_bfloat16*>(y);
+  a.w_pre = w_pre;
+  a.w_post = w_post;
+  a.gate = gate;
+  a.h_out = h_out;
+  a.n = static_cast<__nv_bfloat16*>(n);
+  a.rstd_pre = rstd_pre;
+  a.rstd_post = rstd_post;
+  a.M = M;
+  a.D = D;
+  a.gate_kind = gate_kind;
+  a.resid_f32 = types & QLORA_F32_RESIDUAL;
+  a.weight_f32 = types & QLORA_F32_WEIGHTS;
+  a.gate_f32 = types & QLORA_F32_GATE;
+  a.eps = eps;
+  a.res_scale = res_scale;
+  a.branch_scale = branch_scale;
+  a.weight_offset = weight_offset;
+  st = cuda_status(launch_residual_norm_fwd(a, static_cast<cudaStream_t>(stream)));
+  if (st == QLORA_OK) count(1);
+  return st;
+}
+
+size_t qlora_residual_norm_workspace_bytes(int64_t M, int D) {
+  if (M < 1 || D < 1 || D > kNormMaxD) return 0;
+  return align256(residual_norm_part_bytes(M, D));
+}
+
+qlora_status qlora_residual_norm_bwd(const void* dn, const void* dh_out, const void* h_out,
+                                     const void* y, const float* rstd_pre, const float* rstd_post,
+                                     const void* w_pre, const void* w_post, const void* gate,
+                                     int gate_kind, int64_t M, int D, int types, float res_scale,
+                                     float branch_scale, float weight_offset, void* dh, void* dy,
+                                     float* dw_pre, float* dw_post, void* dgate, void* ws,
+                                     size_t ws_bytes, qlora_stream_t stream) {
+  if (!dh || (!dn && !dh_out)) return QLORA_ERR_NULL;
+  if (w_pre ? (!dn || !h_out || !rstd_pre) : (dn || dw_pre)) return QLORA_ERR_NULL;
+  if (w_post && (!y || !rstd_post || !dy)) return QLORA_ERR_NULL;
+  if (!w_post && dw_post) return QLORA_ERR_NULL;
+  if (gate_kind != QLORA_GATE_NONE && (!gate || !dy)) return QLORA_ERR_NULL;
+  if (dgate && !y) return QLORA_ERR_NULL;
+  if (M < 0 || D < 1 || D > kNormMaxD || gate_kind < QLORA_GATE_NONE ||
+      gate_kind > QLORA_GATE_FULL || (types & ~7) ||
+      (gate_kind == QLORA_GATE_NONE && (gate || dgate)))
+    return QLORA_ERR_SHAPE;
+  for (const void* p :
+       {dn, dh_out, h_out, y, static_cast<const void*>(rstd_pre),
+        static_cast<const void*>(rstd_post), w_pre, w_post, gate, static_cast<const void*>(dh),
+        static_cast<const void*>(dy), static_cast<const void*>(dw_pre),
+        static_cast<const void*>(dw_post), static_cast<const void*>(dgate),
+        static_cast<const void*>(ws)})
+    if (!aligned16(p)) return QLORA_ERR_ALIGN;
+  const bool columns = dw_pre || dw_post || (dgate && gate_kind == QLORA_GATE_CHANNEL);
+  if (columns && M > 0 && (!ws || ws_bytes < qlora_residual_norm_workspace_bytes(M, D)))
+    return QLORA_ERR_WORKSPACE;
+  int dev;
+  qlora_status st = current_device(&dev);
+  if (st != QLORA_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (M == 0) {  // sums over no tokens
+    for (void* p : {static_cast<void*>(dw_pre), static_cast<void*>(dw_post),
+                    gate_kind == QLORA_GATE_CHANNEL ? dgate : nullptr})
+      if (p && (st = cuda_status(cudaMemsetAsync(p, 0, D * 4ull, s))) != QLORA_OK) return st;
+    return QLORA_OK;
+  }
+  ResidualNormBwd a = {};
+  a.dn = static_cast<const __nv_bfloat16*>(dn);
+  a.dh_out = dh_out;
+  a.h_out = h_out;
+  a.y = static_cast<const __nv_bfloat16*>(y);
+  a.rstd_pre = rstd_pre;
+  a.rstd_post = rstd_post;
+  a.w_pre = w_pre;
+  a.w_post = w_post;
+  a.gate = gate;
+  a.dh = dh;
+  a.dy = static_cast<__nv_bfloat16*>(dy);
+  a.dw_pre = dw_pre;
+  a.dw_post = dw_post;
+  a.dgate = dgate;
+  a.part = static_cast<float*>(ws);
+  a.M = M;
+  a.D = D;
+  a.gate_kind = gate_kind;
+  a.resid_f32 = types & QLORA_F32_RESIDUAL;
+  a.weight_f32 = types & QLORA_F32_WEIGHTS;
+  a.gate_f32 = types & QLORA_F32_GATE;
+  a.res_scale = res_scale;
+  a.branch_scale = branch_scale;
+  a.weight_offset = weight_offset;
+  int n = 0;
+  st = cuda_status(launch_residual_norm_bwd(a, s, &n));
+  if (st == QLORA_OK) count(n);
+  return st;
+}
+
+qlora_status qlora_rope_phase(int rotary_dim, double base, int kind, double factor, double low,
+                              double high, double original, uint64_t* phase, float* scale) {
+  if (!phase || !scale) return QLORA_ERR_NULL;
+  const int rd = rotary_dim;
+  if (rd < 2 || rd > 2048 || rd % 2 || !(base > 1.0) || !finite_f(base) ||
+      kind < QLORA_ROPE_PLAIN || kind > QLORA_ROPE_RAMP)
+    return QLORA_ERR_SHAPE;
+  if (kind != QLORA_ROPE_PLAIN && (!(factor >= 1.0) || !finite_f(factor))) return QLORA_ERR_SHAPE;
+  if (kind == QLORA_ROPE_BASE && rd < 4) return QLORA_ERR_SHAPE;
+  if (kind >= QLORA_ROPE_BANDS &&
+      (!(low > 0.0) || !(high > low) || !finite_f(high) || !(original > 0.0) ||
+       !finite_f(original)))
+    return QLORA_ERR_SHAPE;
+  // 64 bits of mantissa: the rounding of a phase to 2^-64 turns per position is its only error
+  // that matters (2^-33 turns at position 2^31).
+  const long double two_pi = 6.283185307179586476925286766559005768L;
+  long double b = base;
+  if (kind == QLORA_ROPE_BASE)
+    b = base * std::pow(static_cast<long double>(factor), static_cast<long double>(rd) / (rd - 2));
+  double l = 0, e = 0;
+  if (kind == QLORA_ROPE_RAMP) {
+    auto pair = [&](double turns) {
+      return rd * std::log(original / (turns * static_cast<double>(two_pi))) /
+             (2.0 * std::log(base));
+    };
+    l = std::max(std::floor(pair(high)), 0.0);
+    e = std::min(std::ceil(pair(low)), rd - 1.0);
+  }
+  for (int i = 0; i < rd / 2; ++i) {
+    long double f = std::pow(b, -2.0L * i / rd);
+    if (kind == QLORA_ROPE_LINEAR) f /= factor;
+    if (kind == QLORA_ROPE_BANDS) {
+      const long double t = (original * f / two_pi - low) / (static_cast<long double>(high) - low);
+      const long double keep = t < 0 ? 0 : (t > 1 ? 1 : t);
+      f *= keep + (1 - keep) / factor;
+    }
+    if (kind == QLORA_ROPE_RAMP) {
+      const double t = (i - l) / std::max(e - l, 1e-3);
+      const long double slow = t < 0 ? 0 : (t > 1 ? 1 : t);
+      f *= 1 - slow + slow / factor;
+    }
+    // f <= 1 radian, so the phase is below 2^62.
+    phase[i] = static_cast<uint64_t>(std::nearbyint(f / two_pi * 18446744073709551616.0L));
+  }
+  *scale = kind == QLORA_ROPE_RAMP ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.f;
+  return QLORA_OK;
+}
+
+qlora_status qlora_rope(const qlora_rope_heads* q, const qlora_rope_heads* k, int64_t B, int64_t S,
+                        int head_dim, int rotary_dim, int f32, const void* positions, int pos64,
+                        int64_t start, const uint64_t* phase, float scale, int interleaved,
+                        int inverse, qlora_stream_t stream) {
+  if (!q || !phase) return QLORA_ERR_NULL;
+  if (B < 0 || S < 0 || (S > 0 && B > (int64_t{1} << 31) / S) || head_dim < 2 ||
+      head_dim > 2048 || rotary_dim < 2 || rotary_dim % 2 || rotary_dim > head_dim)
+    return QLORA_ERR_SHAPE;
+  RopeArgs a = {};
+  const int e = f32 ? 4 : 2;
+  int heads = 0;
+  bool in_place = true;
+  for (int i = 0; i < 2; ++i) {
+    const qlora_rope_heads* h = i == 0 ? q : k;
+    if (!h) continue;
+    if (!h->x || !h->out) return QLORA_ERR_NULL;
+    if (h->heads < 1 || h->heads > 4096 || h->x_batch < 0 || h->x_token < 0 || h->x_head < 0 ||
+        h->out_batch < 0 || h->out_token < 0 || h->out_head < 0)
+      return QLORA_ERR_SHAPE;
+    if (reinterpret_cast<uintptr_t>(h->x) % e || reinterpret_cast<uintptr_t>(h->out) % e)
+      return QLORA_ERR_ALIGN;
+    const bool same = h->x == h->out;
+    if (same && (h->x_batch != h->out_batch || h->x_token != h->out_token ||
+                 h->x_head != h->out_head))
+      return QLORA_ERR_SHAPE;
+    if (i == 1 && same != in_place) return QLORA_ERR_SHAPE;  // both in place, or neither
+    in_place = same;
+    heads += h->heads;
+    a.t[i] = RopeHeads{h->x,       h->out,       h->x_batch, h->x_token,
+                       h->x_head, h->out_batch, h->out_token, h->out_head, h->heads};
+  }
+  if (heads > 4096) return QLORA_ERR_SHAPE;
+  if (reinterpret_cast<uintptr_t>(phase) % 8 ||
+      reinterpret_cast<uintptr_t>(positions) % (pos64 ? 8 : 4))
+    return QLORA_ERR_ALIGN;
+  if (B == 0 || S == 0) return QLORA_OK;
+  int dev;
+  qlora_status st = current_device(&dev);
+  if (st != QLORA_OK) return st;
+  a.phase = phase;
+  a.positions = positions;
+  a.start = start;
+  a.M = B * S;
+  a.S = S;
+  a.head_dim = head_dim;
+  a.rotary_dim = rotary_dim;
+  a.f32 = f32 != 0;
+  a.pos64 = pos64 != 0;
+  a.interleaved = interleaved != 0;
+  a.inverse = inverse != 0;
+  a.copy = !in_place;
+  a.scale = scale;
+  st = cuda_status(launch_rope(a, static_cast<cudaStream_t>(stream)));
+  if (st == QLORA_OK) count(1);
+  return st;
+}
+
+int64_t qlora_adamw_blocks(const qlora_adamw_tensor* tensors, int count) {
+  if (!tensors || count < 1) return 0;
+  int64_t blocks = 0;
+  for (int i = 0; i < count; ++i) {
+    if (tensors[i].n < 0) return 0;
+    blocks += tensors[i].n / kAdamBlock + (tensors[i].n % kAdamBlock != 0);
+  }
+  return blocks;
+}
+
+size_t qlora_adamw_workspace_bytes(int count) {
+  if (count < 1) return 0;
+  const size_t launches = (static_cast<size_t>(count) + kAdamTensors - 1) / kAdamTensors;
+  return align256(launches * kAdamNormCtas * sizeof(double));
+}
+
+qlora_status qlora_adamw_step(const qlora_adamw_tensor* tensors, int count_,
+                              const qlora_adamw_config* config, void* m, void* v, float* m_scale,
+                              float* v_scale, void* state, void* ws, size_t ws_bytes,
+                              qlora_stream_t stream) {
+  if (!tensors || !config || !m || !v || !state) return QLORA_ERR_NULL;
+  const qlora_adamw_config& c = *config;
+  if (count_ < 1 || (c.bits != 8 && c.bits != 32)) return QLORA_ERR_SHAPE;
+  if (c.bits == 8 ? (!m_scale || !v_scale) : (m_scale || v_scale)) return QLORA_ERR_NULL;
+  if (!finite_f(c.lr) || !finite_f(c.grad_scale) || !(c.beta1 >= 0.0 && c.beta1 < 1.0) ||
+      !(c.beta2 >= 0.0 && c.beta2 < 1.0) || !(c.eps >= 0.0) || !finite_f(c.eps) ||
+      !(c.max_norm >= 0.0))
+    return QLORA_ERR_SHAPE;
+  for (int i = 0; i < count_; ++i) {
+    const qlora_adamw_tensor& t = tensors[i];
+    if (t.n < 0 || t.n > (int64_t{1} << 38) || (t.master && t.param_f32)) return QLORA_ERR_SHAPE;
+    if (t.n == 0) continue;
+    if (!t.p || !t.grad) return QLORA_ERR_NULL;
+    if (!aligned16(t.p) || !aligned16(t.master) || !aligned16(t.grad)) return QLORA_ERR_ALIGN;
+  }
+  for (const void* p : {static_cast<const void*>(m), static_cast<const void*>(v),
+                        static_cast<const void*>(m_scale), static_cast<const void*>(v_scale),
+                        static_cast<const void*>(state), static_cast<const void*>(ws)})
+    if (!aligned16(p)) return QLORA_ERR_ALIGN;
+  if (reinterpret_cast<uintptr_t>(c.lr_device) % 4) return QLORA_ERR_ALIGN;
+  const bool use_norm = c.max_norm > 0.0 || c.check_finite;
+  if (use_norm && (!ws || ws_bytes < qlora_adamw_workspace_bytes(count_)))
+    return QLORA_ERR_WORKSPACE;
+  int dev;
+  qlora_status st = current_device(&dev);
+  if (st != QLORA_OK) return st;
+
+  AdamArgs a = {};
+  a.m = m;
+  a.v = v;
+  a.m_scale = m_scale;
+  a.v_scale = v_scale;
+  a.state = state;
+  a.part = static_cast<double*>(ws);
+  a.lr_dev = c.lr_device;
+  a.lr = static_cast<float>(c.lr);
+  a.b1 = static_cast<float>(c.beta1);
+  a.b2 = static_cast<float>(c.beta2);
+  a.one_b1 = static_cast<float>(1.0 - c.beta1);
+  a.one_b2 = static_cast<float>(1.0 - c.beta2);
+  a.eps = static_cast<float>(c.eps);
+  a.grad_scale = static_cast<float>(c.grad_scale);
+  a.max_norm = static_cast<float>(c.max_norm);
+  a.b1d = c.beta1;
+  a.b2d = c.beta2;
+  a.seed = c.seed;
+  a.bits8 = c.bits == 8;
+  a.use_norm = use_norm;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+
+  // Launches of up to kAdamTensors tensors: first every launch's norm, then every launch's step.
+  for (int pass = use_norm ? 0 : 1; pass < 2; ++pass) {
+    int64_t first = 0;
+    int part = 0;
+    for (int i = 0; i < count_; i += kAdamTensors) {
+      AdamTable table;
+      a.tensors = 0;
+      int64_t blocks = 0;
+      const int end = std::min(count_, i + kAdamTensors);
+      for (int j = i; j < end; ++j) {
+        const qlora_adamw_tensor& t = tensors[j];
+        if (t.n == 0) continue;
+        AdamTensor& d = table.t[a.tensors++];
+        d.p = t.p;
+        d.master = t.master;
+        d.g = t.grad;
+        d.n = t.n;
+        d.block0 = static_cast<uint32_t>(blocks);
+        d.flags = (t.param_f32 ? 1u : 0u) | (t.grad_f32 ? 2u : 0u);
+        d.lr_scale = t.lr_scale;
+        d.weight_decay = t.weight_decay;
+        blocks += (t.n + kAdamBlock - 1) / kAdamBlock;
+        if (blocks > 0x7FFFFFFF) return QLORA_ERR_SHAPE;
+      }
+      a.blocks = static_cast<uint32_t>(blocks);
+      a.first_block = first;
+      a.last = end == count_;
+      a.part_first = part;
+      part += adam_norm_ctas(a.blocks);
+      a.part_count = part;
+      st = cuda_status(pass == 0 ? launch_adam_norm(table, a, s) : launch_adam_step(table, a, s));
+      if (st != QLORA_OK) return st;
+      count(1);
+      first += blocks;
+    }
+  }
+  return QLORA_OK;
+}
+
+qlora_status qlora_adamw_moments(const void* m, const void* v, const float* m_scale,
+                                 const float* v_scale, int64_t blocks, int out_f32, void* m_out,
+                                 void* v_out, qlora_stream_t stream) {
+  if (!m || !v || !m_scale || !v_scale || !m_out || !v_out) return QLORA_ERR_NULL;
+  if (blocks < 0) return QLORA_ERR_SHAPE;
+  for (const void* p : {m, v, static_cast<const void*>(m_scale), static_cast<const void*>(v_scale),
+                        static_cast<const void*>(m_out), static_cast<const void*>(v_out)})
+    if (!aligned16(p)) return QLORA_ERR_ALIGN;
+  if (blocks == 0) return QLORA_OK;
+  int dev;
+  qlora_status st = current_device(&dev);
+  if (st != QLORA_OK) return st;
+  AdamArgs a = {};
+  a.m = const_cast<void*>(m);
+  a.v = const_cast<void*>(v);
+  a.m_scale = const_cast<float*>(m_scale);
+  a.v_scale = const_cast<float*>(v_scale);
+  st = cuda_status(launch_adam_moments(a, blocks, m_out, v_out, out_f32 != 0,
+                                       static_cast<cudaStream_t>(stream)));
+  if (st == QLORA_OK) count(1);
+  return st;
+}
+
 size_t qlora_lm_head_ce_workspace_bytes(int M, int V, int K, int chunk) {
   if (M < 1 || V < 128 || V % 64 || K < 128 || K % 64) return 0;
   const int c = chunk < 1 || chunk > M ? M : chunk;
