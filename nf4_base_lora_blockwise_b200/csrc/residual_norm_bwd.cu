@@ -1,0 +1,394 @@
+// residual_norm_bwd.cu -- the backward of the residual norm; the formulas and the way rows are read
+// are described in residual_norm.cu.  With everything constant over a row taken out of its sums
+// (h, y as stored; v the combined weights of the branch; k a token's gate or 1):
+//   q = sum_c dn w_pre h,   G = dh' + r_h dn w_pre - h (r_h^3 q / D)
+//   p = sum_c (G y) v g,    dy = (br k r_y) G v g - y (br k r_y^3 p / D)
+//   dw_pre += (dn h) r_h,   S += (G y) (r_y k g),   a token's dgate = br r_y p,
+// v without the gate for a whole gate g, whose dgate is (G y) v br r_y.
+#include "residual_norm.cuh"
+
+namespace qlora {
+
+namespace {
+
+// Streams of the backward: dn, h', dh', y, then a whole gate.
+template <typename R, int NV>
+struct BwdSlots {
+  static constexpr int GR = sizeof(R) == 4 ? 2 : 1;
+  static constexpr int DN = 0, H = NV, DH = H + NV * GR, Y = DH + NV * GR, GATE = Y + NV;
+};
+
+// DW: with the weights' and the channel gate's gradients.  Each thread sums its own columns over
+// its group's rows in registers: dw_pre, and S, from which dw_post = br gate S and dgate =
+// br (w_post + o) S for a channel gate, both constant over m.  The CTA's sums go to `part` for
+// column_sum_kernel, which adds them in a fixed order: the results do not depend on timing.
+// T: threads at most; 512 leave the 128 registers that the sums and a row's data take.  WS: with the
+// weights staged; GF: with a whole gate.
+template <typename R, int T, bool ALIGNED, bool DW, bool WS, bool GF>
+__global__ void __launch_bounds__(T, 1)
+    residual_norm_bwd_kernel(const __grid_constant__ ResidualNormBwd a,
+                             const __grid_constant__ Ring ring) {
+  constexpr int RB = sizeof(R), NV = 2;
+  using S = BwdSlots<R, NV>;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  __shared__ __align__(16) float buf[4][kSumBuf];
+  const uint32_t smem = smem_u32(smem_raw);
+  const Lane<NV> l = lane_of<NV, T>(ring, smem, a.D);
+  pdl_wait();  // the previous kernel's outputs are complete
+  pdl_trigger();
+  const float inv_d = 1.f / static_cast<float>(a.D);
+  const bool gate_c = a.gate_kind == kGateChannel;
+  const bool post = a.w_post != nullptr;
+  const bool wide = post || gate_c;
+  const bool need_y = a.dy && (post || a.dgate);
+  const bool token_sum = a.dgate && a.gate_kind == kGateToken;
+  Weights w;
+  w.w_pre = a.w_pre;
+  w.w_post = a.w_post;
+  w.gate = gate_c ? a.gate : nullptr;
+  w.weight_f32 = a.weight_f32;
+  w.gate_f32 = a.gate_f32;
+  w.offset = a.weight_offset;
+  w.D = a.D;
+  f2 s_pre[DW ? NV : 1][4], s_post[DW ? NV : 1][4];
+#pragma unroll
+  for (int j = 0; j < (DW ? NV : 1); ++j)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s_pre[j][k] = s_post[j][k] = both(0.f);
+
+  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;
+  RowAt r, next;
+  r.total = next.total = a.M * a.D;
+  r.D = next.D = a.D;
+  int64_t m = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  advance(r, m, a.M);
+  if constexpr (ALIGNED) clear_slots<NV, T>(ring, l, r);
+  // Four copy groups a row, in the order of their use: dn, h', dh', then y and a whole gate.
+  auto start_dn = [&](const RowAt& q) {
+    if (a.w_pre) issue<2, NV, T, ALIGNED, 0, S::DN>(a.dn, l, q);
+    commit_copies();
+  };
+  auto start_h = [&](const RowAt& q) {
+    if (a.w_pre) issue<RB, NV, T, ALIGNED, 1, S::H>(a.h_out, l, q);
+    commit_copies();
+  };
+  auto start_dh = [&](const RowAt& q) {
+    if (a.dh_out) issue<RB, NV, T, ALIGNED, 2, S::DH>(a.dh_out, l, q);
+    commit_copies();
+  };
+  auto start_y = [&](const RowAt& q) {
+    if (need_y) issue<2, NV, T, ALIGNED, 3, S::Y>(a.y, l, q);
+    if constexpr (GF) issue_gate<NV, T, ALIGNED, 4, S::GATE>(a.gate, ring, l, q);
+    commit_copies();
+  };
+  start_dn(r);
+  start_h(r);
+  start_dh(r);
+  start_y(r);
+  if constexpr (WS) stage_weights<ALIGNED>(w, ring, smem_raw, wide);
+  clear_sums(buf, 4);
+  __syncthreads();
+
+  // A row's scalars, read a round ahead: 1 / rms of h' and of y (1 without w_post; 0 without a
+  // row), a token's gate or 1.
+  struct Scalars {
+    float rh, ry, token;
+  };
+  auto scalars = [&](const RowAt& q, int64_t at) {
+    Scalars s = {0.f, 0.f, 1.f};
+    if (q.row) {
+      if (a.w_pre) s.rh = a.rstd_pre[at];
+      s.ry = post ? a.rstd_post[at] : 1.f;
+      if (a.gate_kind == kGateToken) s.token = load_either1(a.gate, a.gate_f32, at);
+    }
+    return s;
+  };
+  Scalars now = scalars(r, m);
+
+  // The same number of rounds for every group, so that a warp's slices stay together.  A round
+  // without a row finds the last row's data (or zeros) and meets it with zero factors.
+  int parity = 0;
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * blockDim.y; base < a.M; base += step) {
+    advance(next, m + step, a.M);
+    const Scalars then = scalars(next, m + step);
+    f2 G[NV][4];
+    if (a.w_pre) {
+      const float rh = now.rh;
+      const f2 rh2 = both(rh);
+      f2 ss = both(0.f);
+      wait_copies<2>();  // dn and h'
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        f2 h[4], v[4];
+        fetch<2, NV, T, ALIGNED, 0, S::DN>(a.dn, l, r, j, G[j]);
+        fetch<RB, NV, T, ALIGNED, 1, S::H>(a.h_out, l, r, j, h);
+        weights8<0, WS, ALIGNED>(w, ring, l, j, v);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const f2 p = mul2(G[j][k], h[k]);
+          if constexpr (DW) s_pre[j][k] = fma2(p, rh2, s_pre[j][k]);
+          ss = fma2(p, v[k], ss);
+          G[j][k] = mul2(G[j][k], v[k]);
+        }
+      }
+      start_dn(next);
+      float s[1] = {sum2(ss)};
+      row_sum<1>(s, buf[parity * 2]);
+      const f2 c2 = both(-s[0] * inv_d * rh * rh * rh);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        f2 h[4];
+        fetch<RB, NV, T, ALIGNED, 1, S::H>(a.h_out, l, r, j, h);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) G[j][k] = fma2(h[k], c2, mul2(G[j][k], rh2));
+      }
+      start_h(next);
+    } else {
+      start_dn(next);
+      start_h(next);
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) G[j][k] = both(0.f);
+    }
+    wait_copies<3>();  // dh'
+    const f2 res = both(a.res_scale);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      f2 d[4];
+      if (a.dh_out) {
+        fetch<RB, NV, T, ALIGNED, 2, S::DH>(a.dh_out, l, r, j, d);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) G[j][k] = add2(G[j][k], d[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) d[k] = mul2(G[j][k], res);
+      put<R, ALIGNED>(static_cast<R*>(a.dh), r, l.c[j], d);
+    }
+    start_dh(next);
+    if (a.dy) {
+      wait_copies<3>();  // y and the gate
+      f2 ss = both(0.f);
+      const float ry = now.ry, token = now.token;
+      const f2 ryk = both(ry * token), bry = both(a.branch_scale * ry);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        f2 y[4], v[4], t[4], g[4];
+        if (need_y) fetch<2, NV, T, ALIGNED, 3, S::Y>(a.y, l, r, j, y);
+        if (wide) {
+          weights8<1, WS, ALIGNED>(w, ring, l, j, v);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) t[k] = mul2(G[j][k], v[k]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) t[k] = G[j][k];
+        }
+        if constexpr (GF) {
+          fetch_gate<NV, T, ALIGNED, 4, S::GATE>(a.gate, ring, l, r, j, g);
+          if (a.dgate) {
+            f2 dg[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) dg[k] = mul2(mul2(t[k], y[k]), bry);
+            if (a.gate_f32)
+              put<float, ALIGNED>(static_cast<float*>(a.dgate), r, l.c[j], dg);
+            else
+              put<__nv_bfloat16, ALIGNED>(static_cast<__nv_bfloat16*>(a.dgate), r, l.c[j], dg);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) t[k] = mul2(t[k], g[k]);
+        }
+        if (need_y) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            ss = fma2(t[k], y[k], ss);
+            if constexpr (DW) {
+              f2 p = mul2(G[j][k], y[k]);
+              if constexpr (GF) p = mul2(p, g[k]);
+              s_post[j][k] = fma2(p, ryk, s_post[j][k]);
+            }
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) G[j][k] = t[k];
+      }
+      float s[1] = {sum2(ss)};
+      if (post || token_sum) {
+        row_sum<1>(s, buf[parity * 2 + 1]);
+        if (token_sum && r.row && threadIdx.x == 0)
+          static_cast<float*>(a.dgate)[m] = a.branch_scale * ry * s[0];
+      }
+      const float brk = a.branch_scale * token;
+      const f2 ct = both(post ? brk * ry : brk), cy = both(-brk * ry * ry * ry * s[0] * inv_d);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) G[j][k] = mul2(G[j][k], ct);
+        if (post) {
+          f2 y[4];
+          fetch<2, NV, T, ALIGNED, 3, S::Y>(a.y, l, r, j, y);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) G[j][k] = fma2(y[k], cy, G[j][k]);
+        }
+        put<__nv_bfloat16, ALIGNED>(a.dy, r, l.c[j], G[j]);
+      }
+    }
+    start_y(next);
+    r = next;
+    now = then;
+    m += step;
+    parity ^= 1;
+  }
+
+  if constexpr (DW) {
+    // The CTA's row groups are added in order through the streams' memory (no copy is in flight: a
+    // row past the last starts none), then one row of sums is left for each gradient.
+    const int rpc = blockDim.y;
+    float* sums = reinterpret_cast<float*>(smem_raw);  // [rpc][2][ld]
+    const int ld = a.part_ld;
+    auto spill = [&](float* d, const f2 (&s)[4]) {
+      float f[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 t = split(s[k]);
+        f[2 * k] = t.x;
+        f[2 * k + 1] = t.y;
+      }
+      store_vec<8>(d, f);
+    };
+    if (rpc > 1) {
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = l.c[j];
+        if (c >= a.D) continue;
+        spill(sums + (threadIdx.y * 2) * ld + c, s_pre[j]);
+        spill(sums + (threadIdx.y * 2 + 1) * ld + c, s_post[j]);
+      }
+      __syncthreads();
+      if (threadIdx.y != 0) return;
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = l.c[j];
+      if (c >= a.D) continue;
+      for (int y = 1; y < rpc; ++y) {
+        float t[8];
+        load_vec<8>(sums + (y * 2) * ld + c, t);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s_pre[j][k] = add2(s_pre[j][k], pair(t[2 * k], t[2 * k + 1]));
+        load_vec<8>(sums + (y * 2 + 1) * ld + c, t);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s_post[j][k] = add2(s_post[j][k], pair(t[2 * k], t[2 * k + 1]));
+      }
+      const int64_t row = blockIdx.x;
+      if (a.dw_pre) spill(a.part + row * ld + c, s_pre[j]);
+      if (a.dw_post || (a.dgate && gate_c)) spill(a.part + (gridDim.x + row) * ld + c, s_post[j]);
+    }
+  }
+}
+
+// Sums over `rows` partial rows in order, 32 columns a CTA: blockDim.y threads a column take every
+// blockDim.y-th row and are added in order.  y = 0: dw_pre; y = 1: S, from which dw_post and a
+// channel gate's dgate.
+constexpr int kSumLanes = 16;
+__global__ void __launch_bounds__(32 * kSumLanes)
+    column_sum_kernel(const float* __restrict__ part, int rows,
+                      const __grid_constant__ ResidualNormBwd a) {
+  __shared__ float s[kSumLanes][33];
+  pdl_wait();
+  pdl_trigger();
+  const int c = blockIdx.x * 32 + threadIdx.x;
+  const bool second = blockIdx.y == 1;
+  const float* p = part + (second ? static_cast<int64_t>(rows) * a.part_ld : 0) + c;
+  float t = 0.f;
+  if (c < a.D) {
+    // Eight loads at a time: the rows are summed in order, whatever their number.
+    int i = threadIdx.y;
+    for (; i + 7 * static_cast<int>(blockDim.y) < rows; i += 8 * blockDim.y) {
+      float q[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) q[k] = p[static_cast<int64_t>(i + k * blockDim.y) * a.part_ld];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) t += q[k];
+    }
+    for (; i < rows; i += blockDim.y) t += p[static_cast<int64_t>(i) * a.part_ld];
+  }
+  s[threadIdx.y][threadIdx.x] = t;
+  __syncthreads();
+  if (threadIdx.y != 0 || c >= a.D) return;
+  float sum = 0.f;
+  for (int i = 0; i < static_cast<int>(blockDim.y); ++i) sum += s[i][threadIdx.x];
+  if (!second) {
+    if (a.dw_pre) a.dw_pre[c] = sum;
+    return;
+  }
+  const bool gate_c = a.gate_kind == kGateChannel;
+  sum *= a.branch_scale;
+  if (a.dw_post)
+    a.dw_post[c] = gate_c ? sum * load_either1(a.gate, a.gate_f32, c) : sum;
+  if (a.dgate && gate_c)
+    static_cast<float*>(a.dgate)[c] =
+        a.w_post ? sum * (load_either1(a.w_post, a.weight_f32, c) + a.weight_offset) : sum;
+}
+
+RowShape bwd_shape(int64_t M, int D) { return row_shape(M, D, D <= 8192 ? 512 : 1024); }
+
+template <typename R, int T, bool ALIGNED, bool DW, bool GF>
+cudaError_t launch_bwd(const ResidualNormBwd& a, const RowShape& s, cudaStream_t st) {
+  Ring ring = {};
+  bool ws;
+  const bool weights = a.w_pre || a.w_post || a.gate_kind == kGateChannel;
+  int smem = plan_ring(a.M, a.D, 5, BwdSlots<R, 2>::GATE, GF, a.gate_f32, weights && T == 512, s,
+                       &ring, &ws);
+  if (DW && s.rpc > 1) {  // the row groups' sums go through the same memory
+    const int sums = s.rpc * 2 * a.part_ld * static_cast<int>(sizeof(float));
+    if (sums > smem) smem = sums;
+  }
+  if constexpr (T == 512) {
+    if (ws)
+      return launch_rows(residual_norm_bwd_kernel<R, T, ALIGNED, DW, true, GF>, s, a, ring, smem,
+                         st);
+  }
+  return launch_rows(residual_norm_bwd_kernel<R, T, ALIGNED, DW, false, GF>, s, a, ring, smem, st);
+}
+template <typename R, int T, bool ALIGNED>
+cudaError_t launch_bwd(const ResidualNormBwd& a, const RowShape& s, bool dw, cudaStream_t st) {
+  if (a.gate_kind == kGateFull)
+    return dw ? launch_bwd<R, T, ALIGNED, true, true>(a, s, st)
+              : launch_bwd<R, T, ALIGNED, false, true>(a, s, st);
+  return dw ? launch_bwd<R, T, ALIGNED, true, false>(a, s, st)
+            : launch_bwd<R, T, ALIGNED, false, false>(a, s, st);
+}
+template <typename R>
+cudaError_t launch_bwd(const ResidualNormBwd& a, const RowShape& s, bool dw, cudaStream_t st) {
+  if (s.threads == 512)
+    return s.aligned ? launch_bwd<R, 512, true>(a, s, dw, st)
+                     : launch_bwd<R, 512, false>(a, s, dw, st);
+  return s.aligned ? launch_bwd<R, 1024, true>(a, s, dw, st)
+                   : launch_bwd<R, 1024, false>(a, s, dw, st);
+}
+
+}  // namespace
+
+size_t residual_norm_part_bytes(int64_t M, int D) {
+  return static_cast<size_t>(2 * bwd_shape(M, D).ctas) * ((D + 7) / 8 * 8) * sizeof(float);
+}
+
+cudaError_t launch_residual_norm_bwd(const ResidualNormBwd& args, cudaStream_t stream, int* n) {
+  ResidualNormBwd a = args;
+  a.part_ld = (a.D + 7) / 8 * 8;
+  const bool second = a.dw_post || (a.dgate && a.gate_kind == kGateChannel);
+  const bool dw = a.dw_pre || second;
+  const RowShape s = bwd_shape(a.M, a.D);
+  const cudaError_t e = a.resid_f32 ? launch_bwd<float>(a, s, dw, stream)
+                                    : launch_bwd<__nv_bfloat16>(a, s, dw, stream);
+  *n = 1;
+  if (e != cudaSuccess || !dw) return e;
+  *n = 2;
+  int lanes = 1;
+  while (lanes < kSumLanes && lanes * 8 < s.ctas) lanes *= 2;
+  return launch_pdl(column_sum_kernel, dim3((a.D + 31) / 32, second ? 2 : 1), dim3(32, lanes), 0,
+                    stream, 1, a.part, static_cast<int>(s.ctas), a);
+}
+
+}  // namespace qlora
