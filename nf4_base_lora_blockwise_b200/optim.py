@@ -9,6 +9,7 @@ import ctypes
 import torch
 
 from . import abi
+from .block import _bind
 from .linear import _ptr
 
 _BLOCK = 256
@@ -94,6 +95,8 @@ class AdamW:
         self._config = abi.AdamWConfig(0.0 if self._lr is not None else lr, betas[0], betas[1],
                                        eps, grad_scale, max_grad_norm or 0.0, _ptr(self._lr),
                                        seed & 0xFFFFFFFF, bits, bool(check_finite))
+        self._has_norm = self._config.max_norm > 0 or bool(check_finite)
+        self._stream = _bind().current_stream
         self._ws = zeros(abi.qlora_adamw_workspace_bytes(count), torch.uint8)
         # What a step passes, marshalled once.
         buffer = lambda t: None if t is None else t.untyped_storage().data_ptr()  # noqa: E731
@@ -127,12 +130,12 @@ class AdamW:
     def step(self):
         """One step on the current stream.  Returns the gradients' norm (a one-element fp32 tensor
         that the next step overwrites), or None where it is not computed."""
-        dev = torch.cuda.current_device()
-        if dev != self.device.index:
+        stream = self._stream(self.device.index)
+        if stream is None:
             raise ValueError(f"AdamW.step: the tensors are on {self.device}, the current device "
-                             f"is {dev}")
-        abi.qlora_adamw_step(*self._args, torch.cuda.current_stream(dev).cuda_stream)
-        return self._norm if self._config.max_norm > 0 or self._config.check_finite else None
+                             f"is {torch.cuda.current_device()}")
+        abi.qlora_adamw_step(*self._args, stream)
+        return self._norm if self._has_norm else None
 
     @property
     def lr(self):
@@ -164,18 +167,8 @@ class AdamW:
             raise ValueError(f"moments: expected fp32 or bf16, got {dtype}")
         if self.m_scale is None:
             return self.m.to(dtype), self.v.to(dtype)
-        dev = torch.cuda.current_device()
-        if dev != self.device.index:
-            raise ValueError(f"AdamW.moments: the tensors are on {self.device}, the current "
-                             f"device is {dev}")
-        m = torch.empty(self.m.numel(), dtype=dtype, device=self.device)
-        v = torch.empty_like(m)
-        if m.numel():
-            abi.qlora_adamw_moments(self.m.data_ptr(), self.v.data_ptr(), self.m_scale.data_ptr(),
-                                    self.v_scale.data_ptr(), self.m_scale.numel(),
-                                    dtype is torch.float32, m.data_ptr(), v.data_ptr(),
-                                    torch.cuda.current_stream(dev).cuda_stream)
-        return m, v
+        return _bind().adamw_moments(self.m, self.v, self.m_scale, self.v_scale,
+                                     dtype is torch.float32)
 
     def state_dict(self):
         """Copies of the moments and the step count."""

@@ -216,3 +216,13 @@ def test_struct_layouts(tmp_path):
     assert got == [ctypes.sizeof(abi.RopeHeads), ctypes.sizeof(abi.AdamWTensor),
                    ctypes.sizeof(abi.AdamWConfig), abi.AdamWConfig.seed.offset,
                    abi.RopeHeads.heads.offset]
+
+
+def test_binding_raises():
+    """The torch binding's errors reach Python as exceptions (it shares torch's C++ runtime)."""
+    b = block._bind()
+    for f in (b.residual_norm_forward, b.residual_norm_backward, b.rope, b.adamw_moments):
+        with pytest.raises(TypeError, match="arguments, got 1"):
+            f(None)
+    with pytest.raises(TypeError):
+        b.current_stream("x")
