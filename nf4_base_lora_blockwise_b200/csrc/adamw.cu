@@ -16,11 +16,15 @@
 // The fp32 operations that lead to a code (moments, root, scale, quotient) are kept unfused and
 // correctly rounded, so that codes do not depend on how the compiler contracts them.
 //
-// Bound by memory.  A warp takes one block of 256 at a time, 8 consecutive elements a lane, so
-// every access is 16 or 32 bytes a lane (8 for codes) and a block's scale is one warp reduction.
+// Bound by memory, with 8-bit moments nearly by instruction issue (18 bytes an element leave about
+// 60 instructions for it).  A warp takes one block of 256 at a time, 8 consecutive elements a lane,
+// so every access is 16 or 32 bytes a lane (8 for codes) and a block's scale is one warp
+// reduction.  Codes are decoded through tables in shared memory; codes below the grid's least value
+// are rare and made by a second pass over the warp's block.
 #include <cuda_bf16.h>
 
 #include <cstdint>
+#include <cstring>
 
 #include "kernels.h"
 #include "ptx.cuh"
@@ -44,32 +48,48 @@ __device__ __forceinline__ uint32_t element_bits(uint32_t word, int64_t e) {
   return mix32((static_cast<uint32_t>(e) ^ (hi * 0x9E3779B1u)) + word);
 }
 
-constexpr int kMBase = 889, kVBase = 1777;  // fp32 bits >> 20 of 1.0 less 127, >> 19 less 255
-constexpr float kMLeast = 1.25f / 65536.f;  // the value of m's code 1
+constexpr uint32_t kMBase = 889, kVBase = 1777;  // fp32 bits of 1.0 >> 20 less 127, >> 19 less 255
+constexpr float kMLeast = 1.25f / 65536.f, kVLeast = 1.125f / 65536.f;  // the values of code 1
 
-__device__ __forceinline__ float decode_m(uint32_t c, float scale) {
-  const uint32_t mag = c & 127u;
-  const float x = mag ? __uint_as_float((mag + kMBase) << 20) : 0.f;
-  return __fmul_rn((c & 128u) ? -x : x, scale);
+// The values of the 256 codes, over the scale (of v: of its root).
+struct CodeTables {
+  float m[256], v[256];
+};
+__device__ __forceinline__ void fill_tables(CodeTables& t) {
+  for (int c = threadIdx.x; c < 256; c += blockDim.x) {
+    const uint32_t mag = c & 127u;
+    const float x = mag ? __uint_as_float((mag + kMBase) << 20) : 0.f;
+    t.m[c] = (c & 128) ? -x : x;
+    t.v[c] = c ? __uint_as_float((static_cast<uint32_t>(c) + kVBase) << 19) : 0.f;
+  }
 }
-__device__ __forceinline__ float decode_v(uint32_t c, float scale) {
-  const float root = __fmul_rn(c ? __uint_as_float((c + kVBase) << 19) : 0.f, scale);
-  return __fmul_rn(root, root);
+// Two consecutive elements' values from byte `k` and `k + 1` of a word of codes.
+__device__ __forceinline__ f2 decode2(const float* table, uint32_t word, int k, f2 scale) {
+  const uint32_t a = (word >> (8 * k)) & 255u, b = (word >> (8 * k + 8)) & 255u;
+  return mul2(pair(table[a], table[b]), scale);
 }
-// Codes for a magnitude x = |m| / scale or sqrt(v) / scale in [0, 1]; r: 16 random bits.
+// Codes of a magnitude x = |m| / scale or sqrt(v) / scale in [0, 1] that is not below the least
+// value; r: 16 random bits.  (A little past 1 the carry still stays within the top code; what a
+// NaN or infinity gives does not matter, its block's scale is not finite.)
 __device__ __forceinline__ uint32_t encode_m(float x, uint32_t r) {
-  if (x < kMLeast) return __fmul_rn(static_cast<float>(r), kMLeast / 65536.f) < x ? 1u : 0u;
-  const uint32_t c = ((__float_as_uint(x) + (r << 4)) >> 20) - kMBase;
-  return c > 127u ? 127u : c;
+  return (__float_as_uint(x) + (r << 4) - (kMBase << 20)) >> 20;
 }
 __device__ __forceinline__ uint32_t encode_v(float x, uint32_t r) {
-  if (!(x > 0.f)) return 0u;
-  const int c = static_cast<int>((__float_as_uint(x) + (r << 3)) >> 19) - kVBase;
-  return c < 1 ? 1u : (c > 255 ? 255u : static_cast<uint32_t>(c));
+  return (__float_as_uint(x) + (r << 3) - (kVBase << 19)) >> 19;
+}
+// ... and of any x.
+__device__ __forceinline__ uint32_t encode_m_any(float x, uint32_t r) {
+  if (x < kMLeast) return __fmul_rn(static_cast<float>(r), kMLeast / 65536.f) < x ? 1u : 0u;
+  return encode_m(x, r);
+}
+__device__ __forceinline__ uint32_t encode_v_any(float x, uint32_t r) {
+  if (x < kVLeast) return x > 0.f ? 1u : 0u;
+  return encode_v(x, r);
 }
 
 // The tensor that block `b` of the launch belongs to.
-__device__ __forceinline__ int tensor_of(const AdamTable& t, int n, uint32_t b) {
+template <int N>
+__device__ __forceinline__ int tensor_of(const AdamTable<N>& t, int n, uint32_t b) {
   int lo = 0, hi = n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -104,10 +124,17 @@ __device__ __forceinline__ double power(double b, int64_t t) {
   return r;
 }
 
+// The factors of the bias corrections of step t.
+__device__ __forceinline__ void corrections(const AdamArgs& a, int64_t t, float* c1, float* c2) {
+  *c1 = static_cast<float>(1.0 / (1.0 - power(a.b1d, t)));
+  *c2 = static_cast<float>(1.0 / sqrt(1.0 - power(a.b2d, t)));
+}
+
 // Sums of squares of the scaled gradients, in 64 bits (no overflow for finite gradients), one a
 // CTA; the last CTA of the list adds them in order and leaves norm and factor in the state.
+template <int N>
 __global__ void __launch_bounds__(kAdamThreads)
-    adam_norm_kernel(const __grid_constant__ AdamTable table, const AdamArgs a) {
+    adam_norm_kernel(const __grid_constant__ AdamTable<N> table, const AdamArgs a) {
   __shared__ double s[kAdamWarps];
   __shared__ bool last;
   pdl_wait();  // the previous kernel's outputs are complete
@@ -165,133 +192,228 @@ __global__ void __launch_bounds__(kAdamThreads)
     const int ok = isfinite(norm);
     st->finite = ok;
     if (!ok) st->skipped += 1;
+    corrections(a, st->step + 1, &st->c1, &st->c2);
     st->ticket = 0;
   }
 }
 
+// What a lane holds of a block: 8 elements' parameters, gradients and moments.
 template <bool BITS8>
-__global__ void __launch_bounds__(kAdamThreads)
-    adam_step_kernel(const __grid_constant__ AdamTable table, const AdamArgs a) {
+struct Held {
+  float p[8], g[8];
+  f2 m[BITS8 ? 1 : 4], v[BITS8 ? 1 : 4];
+  uint2 cm, cv;
+  float sm, sv;
+};
+
+// The parameter that the step is taken on: the master copy, or p itself.
+__device__ __forceinline__ bool lead_f32(const AdamTensor& t) { return t.master || (t.flags & 1u); }
+__device__ __forceinline__ void* lead(const AdamTensor& t) { return t.master ? t.master : t.p; }
+
+template <bool BITS8>
+__device__ __forceinline__ void load_block(const AdamTensor& t, const AdamArgs& a, uint32_t b,
+                                           int lane, Held<BITS8>& h) {
+  const int64_t i = static_cast<int64_t>(b - t.block0) * kAdamBlock + lane * 8;
+  const int64_t gb = a.first_block + b, e0 = gb * kAdamBlock + lane * 8;
+  load8(t.g, t.flags & 2u, i, t.n, h.g);
+  load8(lead(t), lead_f32(t), i, t.n, h.p);
+  if constexpr (BITS8) {
+    h.cm = *reinterpret_cast<const uint2*>(static_cast<uint8_t*>(a.m) + e0);
+    h.cv = *reinterpret_cast<const uint2*>(static_cast<uint8_t*>(a.v) + e0);
+    h.sm = a.m_scale[gb];
+    h.sv = a.v_scale[gb];
+  } else {
+    float m[8], v[8];
+    load_vec<8>(static_cast<const float*>(a.m) + e0, m);
+    load_vec<8>(static_cast<const float*>(a.v) + e0, v);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      h.m[k] = pair(m[2 * k], m[2 * k + 1]);
+      h.v[k] = pair(v[2 * k], v[2 * k + 1]);
+    }
+  }
+}
+
+template <bool BITS8, int N>
+__global__ void __launch_bounds__(kAdamThreads, 4)
+    adam_step_kernel(const __grid_constant__ AdamTable<N> table,
+                     const __grid_constant__ AdamArgs a) {
   __shared__ float sc[2];
   __shared__ int64_t step_s;
+  __shared__ CodeTables codes;
+  if constexpr (BITS8) fill_tables(codes);
   pdl_wait();  // the previous kernel's outputs are complete
   pdl_trigger();
   AdamState* st = static_cast<AdamState*>(a.state);
   if (a.use_norm && !st->finite) return;  // the whole step is left out
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t end = share(a.blocks, blockIdx.x + 1);
+  uint32_t b = share(a.blocks, blockIdx.x) + warp;
+  int ti = 0;
+  Held<BITS8> h;
+  if (b < end) {  // the first block is on its way while the corrections are worked out
+    ti = tensor_of(table, a.tensors, b);
+    load_block(table.t[ti], a, b, lane, h);
+  }
   if (threadIdx.x == 0) {
     const int64_t t = st->step + 1;
     step_s = t;
-    sc[0] = static_cast<float>(1.0 / (1.0 - power(a.b1d, t)));
-    sc[1] = static_cast<float>(1.0 / sqrt(1.0 - power(a.b2d, t)));
+    if (a.use_norm) {
+      sc[0] = st->c1;
+      sc[1] = st->c2;
+    } else {
+      corrections(a, t, &sc[0], &sc[1]);
+    }
   }
   __syncthreads();
-  const float c1 = sc[0], c2 = sc[1];
+  const float c1 = sc[0];
   const float factor = a.use_norm ? st->factor : a.grad_scale;
   const float lr = a.lr_dev ? *a.lr_dev : a.lr;
   const uint32_t word = mix32(mix32(a.seed) + static_cast<uint32_t>(step_s));
-  const uint32_t word2 = mix32(mix32(a.seed ^ 0x55555555u) + static_cast<uint32_t>(step_s));
+  const f2 c2 = both(sc[1]), eps = both(a.eps), fac = both(factor);
 
-  const uint32_t end = share(a.blocks, blockIdx.x + 1);
-  uint32_t b = share(a.blocks, blockIdx.x) + warp;
-  if (b < end) {
-    int ti = tensor_of(table, a.tensors, b);
-    for (; b < end; b += kAdamWarps) {
-      while (ti + 1 < a.tensors && table.t[ti + 1].block0 <= b) ++ti;
-      const AdamTensor& t = table.t[ti];
-      const int64_t i = static_cast<int64_t>(b - t.block0) * kAdamBlock + lane * 8;
-      const int64_t gb = a.first_block + b;          // block of the list
-      const int64_t e0 = gb * kAdamBlock + lane * 8;  // element of the list
-      float g[8], p[8], m[8], v[8];
-      load8(t.g, t.flags & 2u, i, t.n, g);
-      const bool p32 = t.master || (t.flags & 1u);
-      float* pf = t.master ? t.master : static_cast<float*>(t.p);
-      load8(p32 ? static_cast<const void*>(pf) : t.p, p32, i, t.n, p);
-      if constexpr (BITS8) {
-        const uint2 cm = reinterpret_cast<const uint2*>(static_cast<uint8_t*>(a.m) + e0)[0];
-        const uint2 cv = reinterpret_cast<const uint2*>(static_cast<uint8_t*>(a.v) + e0)[0];
-        const float sm = a.m_scale[gb], sv = a.v_scale[gb];
+  while (b < end) {
+    const AdamTensor& t = table.t[ti];
+    const int64_t i = static_cast<int64_t>(b - t.block0) * kAdamBlock + lane * 8;
+    const int64_t gb = a.first_block + b;           // block of the list
+    const int64_t e0 = gb * kAdamBlock + lane * 8;  // element of the list
+    const float rate = lr * t.lr_scale;
+    const f2 keep = both(1.f - rate * t.weight_decay), move = both(-rate * c1);
+    float m[8], root[8], p[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          m[k] = decode_m(((k < 4 ? cm.x : cm.y) >> (8 * (k & 3))) & 255u, sm);
-          v[k] = decode_v(((k < 4 ? cv.x : cv.y) >> (8 * (k & 3))) & 255u, sv);
-        }
+    for (int k = 0; k < 4; ++k) {
+      const f2 g = mul2(pair(h.g[2 * k], h.g[2 * k + 1]), fac);
+      f2 mk, vk;
+      if constexpr (BITS8) {
+        mk = decode2(codes.m, k < 2 ? h.cm.x : h.cm.y, 2 * (k & 1), both(h.sm));
+        vk = decode2(codes.v, k < 2 ? h.cv.x : h.cv.y, 2 * (k & 1), both(h.sv));
+        vk = mul2(vk, vk);
       } else {
-        load_vec<8>(static_cast<const float*>(a.m) + e0, m);
-        load_vec<8>(static_cast<const float*>(a.v) + e0, v);
+        mk = h.m[k];
+        vk = h.v[k];
       }
-      const float rate = lr * t.lr_scale;
-      const float keep = 1.f - rate * t.weight_decay, move = rate * c1;
-      float root[8];
+      mk = add2(mul2(mk, both(a.b1)), mul2(g, both(a.one_b1)));
+      vk = add2(mul2(vk, both(a.b2)), mul2(mul2(g, g), both(a.one_b2)));
+      const float2 v = split(vk), mm = split(mk);
+      m[2 * k] = mm.x;
+      m[2 * k + 1] = mm.y;
+      root[2 * k] = sqrtf(v.x);
+      root[2 * k + 1] = sqrtf(v.y);
+      const float2 d = split(fma2(pair(root[2 * k], root[2 * k + 1]), c2, eps));
+      const f2 u = pair(__fdividef(mm.x, d.x), __fdividef(mm.y, d.y));
+      const float2 q = split(fma2(u, move, mul2(pair(h.p[2 * k], h.p[2 * k + 1]), keep)));
+      p[2 * k] = q.x;
+      p[2 * k + 1] = q.y;
+      if constexpr (!BITS8) {
+        h.m[k] = mk;
+        h.v[k] = vk;
+      }
+    }
+    // Parameters.
+    const bool whole = i + 8 <= t.n;
+    if (lead_f32(t)) {
+      float* pf = static_cast<float*>(lead(t));
+      if (whole) {
+        store_vec<8>(pf + i, p);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (i + k < t.n) pf[i + k] = p[k];
+      }
+    } else {
+      const uint32_t word2 =
+          mix32(mix32(a.seed ^ 0x55555555u) + static_cast<uint32_t>(step_s));
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float gk = __fmul_rn(g[k], factor);
-        m[k] = __fadd_rn(__fmul_rn(m[k], a.b1), __fmul_rn(gk, a.one_b1));
-        v[k] = __fadd_rn(__fmul_rn(v[k], a.b2), __fmul_rn(__fmul_rn(gk, gk), a.one_b2));
-        root[k] = sqrtf(v[k]);
-        p[k] = p[k] * keep - move * __fdividef(m[k], root[k] * c2 + a.eps);
+        // 16 random bits added below the bf16 ones; a NaN or infinity keeps its bits.
+        const uint32_t w = __float_as_uint(p[k]);
+        if ((w & 0x7F800000u) != 0x7F800000u)
+          p[k] = __uint_as_float((w + (element_bits(word2, e0 + k) & 0xFFFFu)) & 0xFFFF0000u);
       }
-      // Parameters.
-      const bool whole = i + 8 <= t.n;
-      if (p32) {
-        if (whole) {
-          store_vec<8>(pf + i, p);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (i + k < t.n) pf[i + k] = p[k];
-        }
+    }
+    if (!(t.flags & 1u)) {
+      __nv_bfloat16* pb = static_cast<__nv_bfloat16*>(t.p);
+      if (whole) {
+        store_vec<8>(pb + i, p);
       } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          // 16 random bits added below the bf16 ones; a NaN or infinity keeps its bits.
-          const uint32_t w = __float_as_uint(p[k]);
-          if ((w & 0x7F800000u) != 0x7F800000u)
-            p[k] = __uint_as_float((w + (element_bits(word2, e0 + k) & 0xFFFFu)) & 0xFFFF0000u);
-        }
+        for (int k = 0; k < 8; ++k)
+          if (i + k < t.n) pb[i + k] = __float2bfloat16_rn(p[k]);
       }
-      if (!(t.flags & 1u)) {
-        __nv_bfloat16* pb = static_cast<__nv_bfloat16*>(t.p);
-        if (whole) {
-          store_vec<8>(pb + i, p);
-        } else {
+    }
+    // The next block's loads go out before this one's codes are made.
+    b += kAdamWarps;
+    if constexpr (!BITS8) {
+      float f[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (i + k < t.n) pb[i + k] = __float2bfloat16_rn(p[k]);
+      for (int s = 0; s < 2; ++s) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 x = split(s == 0 ? h.m[k] : h.v[k]);
+          f[2 * k] = x.x;
+          f[2 * k + 1] = x.y;
         }
+        store_vec<8>(static_cast<float*>(s == 0 ? a.m : a.v) + e0, f);
       }
-      // Moments.
-      if constexpr (BITS8) {
-        uint32_t am = 0, ar = 0;  // as bits: a NaN is the largest, and the block's scale
+    }
+    if (b < end) {
+      while (ti + 1 < a.tensors && table.t[ti + 1].block0 <= b) ++ti;
+      load_block(table.t[ti], a, b, lane, h);
+    }
+    if constexpr (BITS8) {
+      uint32_t am = 0, ar = 0;  // as bits: a NaN is the largest, and the block's scale
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          am = max(am, __float_as_uint(m[k]) & 0x7FFFFFFFu);
-          ar = max(ar, __float_as_uint(root[k]) & 0x7FFFFFFFu);
-        }
-        am = __reduce_max_sync(0xFFFFFFFFu, am);
-        ar = __reduce_max_sync(0xFFFFFFFFu, ar);
-        if (am < 0x00800000u) am = 0;  // below the normal numbers: a block of zeros
-        if (ar < 0x00800000u) ar = 0;
-        const float sm = __uint_as_float(am), sv = __uint_as_float(ar);
-        const float im = am ? __fdiv_rn(1.f, sm) : 0.f, iv = ar ? __fdiv_rn(1.f, sv) : 0.f;
-        uint32_t cm[2] = {0, 0}, cv[2] = {0, 0};
+      for (int k = 0; k < 8; ++k) {
+        am = max(am, __float_as_uint(m[k]) & 0x7FFFFFFFu);
+        ar = max(ar, __float_as_uint(root[k]) & 0x7FFFFFFFu);
+      }
+      am = __reduce_max_sync(0xFFFFFFFFu, am);
+      ar = __reduce_max_sync(0xFFFFFFFFu, ar);
+      if (am < 0x00800000u) am = 0;  // below the normal numbers: a block of zeros
+      if (ar < 0x00800000u) ar = 0;
+      const float sm = __uint_as_float(am), sv = __uint_as_float(ar);
+      const f2 im = both(am ? __fdiv_rn(1.f, sm) : 0.f), iv = both(ar ? __fdiv_rn(1.f, sv) : 0.f);
+      const uint32_t lo = static_cast<uint32_t>(e0);
+      const uint32_t hi = static_cast<uint32_t>(static_cast<uint64_t>(e0) >> 32) * 0x9E3779B1u;
+      uint32_t cm[2] = {0, 0}, cv[2] = {0, 0};
+      auto make = [&](auto em, auto ev) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t r = element_bits(word, e0 + k);
-          const uint32_t c = encode_m(__fmul_rn(fabsf(m[k]), im), r & 0xFFFFu) |
-                             (m[k] < 0.f ? 128u : 0u);
-          cm[k >> 2] |= c << (8 * (k & 3));
-          cv[k >> 2] |= encode_v(__fmul_rn(root[k], iv), r >> 16) << (8 * (k & 3));
+        for (int k = 0; k < 8; k += 2) {
+          const float2 x = split(mul2(pair(fabsf(m[k]), fabsf(m[k + 1])), im));
+          const float2 y = split(mul2(pair(root[k], root[k + 1]), iv));
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const uint32_t r = mix32(((lo + k + q) ^ hi) + word);
+            const uint32_t c = (em(q ? x.y : x.x, r & 0xFFFFu) & 127u) |
+                               ((__float_as_uint(m[k + q]) >> 24) & 128u);
+            const uint32_t d = ev(q ? y.y : y.x, r >> 16) & 255u;
+            if ((k + q) & 3) {
+              cm[k >> 2] |= c << (8 * ((k + q) & 3));
+              cv[k >> 2] |= d << (8 * ((k + q) & 3));
+            } else {
+              cm[k >> 2] = c;
+              cv[k >> 2] = d;
+            }
+          }
         }
-        reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.m) + e0)[0] = make_uint2(cm[0], cm[1]);
-        reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v) + e0)[0] = make_uint2(cv[0], cv[1]);
-        if (lane == 0) {
-          a.m_scale[gb] = sm;
-          a.v_scale[gb] = sv;
-        }
-      } else {
-        store_vec<8>(static_cast<float*>(a.m) + e0, m);
-        store_vec<8>(static_cast<float*>(a.v) + e0, v);
+      };
+      // The least of the block's |m| and roots, against the grids' least values.
+      float lm = fabsf(m[0]), lr_ = root[0];
+#pragma unroll
+      for (int k = 1; k < 8; ++k) {
+        lm = fminf(lm, fabsf(m[k]));
+        lr_ = fminf(lr_, root[k]);
+      }
+      // (A little above, for the rounding of the quotients.)
+      if (__any_sync(0xFFFFFFFFu, !(lm > 1.001f * kMLeast * sm && lr_ > 1.001f * kVLeast * sv)))
+        make(encode_m_any, encode_v_any);
+      else
+        make(encode_m, encode_v);
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.m) + e0) = make_uint2(cm[0], cm[1]);
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v) + e0) = make_uint2(cv[0], cv[1]);
+      if (lane == 0) {
+        a.m_scale[gb] = sm;
+        a.v_scale[gb] = sv;
       }
     }
   }
@@ -309,6 +431,9 @@ template <typename T>
 __global__ void __launch_bounds__(kAdamThreads)
     adam_moments_kernel(const uint8_t* mc, const uint8_t* vc, const float* ms, const float* vs,
                         int64_t vectors, T* m_out, T* v_out) {
+  __shared__ CodeTables codes;
+  fill_tables(codes);
+  __syncthreads();
   pdl_wait();
   pdl_trigger();
   const int64_t stride = static_cast<int64_t>(gridDim.x) * kAdamThreads;
@@ -319,9 +444,14 @@ __global__ void __launch_bounds__(kAdamThreads)
     const float sm = ms[i / (kAdamBlock / 8)], sv = vs[i / (kAdamBlock / 8)];
     float m[8], v[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      m[k] = decode_m(((k < 4 ? cm.x : cm.y) >> (8 * (k & 3))) & 255u, sm);
-      v[k] = decode_v(((k < 4 ? cv.x : cv.y) >> (8 * (k & 3))) & 255u, sv);
+    for (int k = 0; k < 4; ++k) {
+      const float2 x = split(decode2(codes.m, k < 2 ? cm.x : cm.y, 2 * (k & 1), both(sm)));
+      const f2 r = decode2(codes.v, k < 2 ? cv.x : cv.y, 2 * (k & 1), both(sv));
+      const float2 y = split(mul2(r, r));
+      m[2 * k] = x.x;
+      m[2 * k + 1] = x.y;
+      v[2 * k] = y.x;
+      v[2 * k + 1] = y.y;
     }
     store_vec<8>(m_out + i * 8, m);
     store_vec<8>(v_out + i * 8, v);
@@ -338,17 +468,37 @@ constexpr int kStepCtas = 148 * 4;
 
 int adam_norm_ctas(uint32_t blocks) { return adam_ctas(blocks, kAdamNormCtas); }
 
-cudaError_t launch_adam_norm(const AdamTable& table, const AdamArgs& a, cudaStream_t stream) {
-  return launch_pdl(adam_norm_kernel, dim3(adam_norm_ctas(a.blocks)), dim3(kAdamThreads), 0,
-                    stream, 1, table, a);
+namespace {
+template <int N>
+AdamTable<N> table_of(const AdamTensor* t, int n) {
+  AdamTable<N> table;
+  std::memcpy(table.t, t, n * sizeof(AdamTensor));
+  return table;
+}
+template <int N>
+cudaError_t launch_norm(const AdamTensor* t, const AdamArgs& a, cudaStream_t stream) {
+  return launch_pdl(adam_norm_kernel<N>, dim3(adam_norm_ctas(a.blocks)), dim3(kAdamThreads), 0,
+                    stream, 1, table_of<N>(t, a.tensors), a);
+}
+template <int N>
+cudaError_t launch_step(const AdamTensor* t, const AdamArgs& a, cudaStream_t stream) {
+  const dim3 grid(adam_ctas(a.blocks, kStepCtas));
+  if (a.bits8)
+    return launch_pdl(adam_step_kernel<true, N>, grid, dim3(kAdamThreads), 0, stream, 1,
+                      table_of<N>(t, a.tensors), a);
+  return launch_pdl(adam_step_kernel<false, N>, grid, dim3(kAdamThreads), 0, stream, 1,
+                    table_of<N>(t, a.tensors), a);
+}
+}  // namespace
+
+cudaError_t launch_adam_norm(const AdamTensor* t, const AdamArgs& a, cudaStream_t stream) {
+  return a.tensors <= kAdamFew ? launch_norm<kAdamFew>(t, a, stream)
+                               : launch_norm<kAdamTensors>(t, a, stream);
 }
 
-cudaError_t launch_adam_step(const AdamTable& table, const AdamArgs& a, cudaStream_t stream) {
-  if (a.bits8)
-    return launch_pdl(adam_step_kernel<true>, dim3(adam_ctas(a.blocks, kStepCtas)), dim3(kAdamThreads), 0,
-                      stream, 1, table, a);
-  return launch_pdl(adam_step_kernel<false>, dim3(adam_ctas(a.blocks, kStepCtas)), dim3(kAdamThreads), 0,
-                    stream, 1, table, a);
+cudaError_t launch_adam_step(const AdamTensor* t, const AdamArgs& a, cudaStream_t stream) {
+  return a.tensors <= kAdamFew ? launch_step<kAdamFew>(t, a, stream)
+                               : launch_step<kAdamTensors>(t, a, stream);
 }
 
 cudaError_t launch_adam_moments(const AdamArgs& a, int64_t blocks, void* m_out, void* v_out,

@@ -442,7 +442,9 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream);
 // ------------------------------ AdamW over many tensors -------------------------------------
 // Blocks of 256 elements are numbered through the list of tensors, each tensor starting one.
 constexpr int kAdamBlock = 256;
-constexpr int kAdamTensors = 512;  // tensors of one launch: 24 KB of kernel parameters
+// Tensors of one launch, which are kernel parameters (24 KB for 512).  A launch pays for the size of
+// its table, so short lists take a short one.
+constexpr int kAdamTensors = 512, kAdamFew = 16;
 struct AdamTensor {
   void* p;            // bf16, or fp32 when param_f32
   float* master;      // fp32 copy or null
@@ -452,8 +454,9 @@ struct AdamTensor {
   uint32_t flags;     // 1: p fp32, 2: g fp32
   float lr_scale, weight_decay;
 };
+template <int N>
 struct AdamTable {
-  AdamTensor t[kAdamTensors];
+  AdamTensor t[N];
 };
 struct AdamArgs {
   int tensors;
@@ -480,12 +483,14 @@ struct AdamState {       // device, zero (or the steps taken so far) before the 
   int32_t skipped;       // steps left out for a norm that was not finite
   uint32_t ticket;       // zero between launches
   int32_t finite;
-  int32_t pad[9];
+  float c1, c2;          // 1 / (1 - b1^t), 1 / sqrt(1 - b2^t) of the next step
+  int32_t pad[7];
 };
 constexpr int kAdamNormCtas = 148 * 8;  // at most: one double of workspace each
 int adam_norm_ctas(uint32_t blocks);
-cudaError_t launch_adam_norm(const AdamTable& table, const AdamArgs& a, cudaStream_t stream);
-cudaError_t launch_adam_step(const AdamTable& table, const AdamArgs& a, cudaStream_t stream);
+// tensors: a.tensors of them.
+cudaError_t launch_adam_norm(const AdamTensor* tensors, const AdamArgs& a, cudaStream_t stream);
+cudaError_t launch_adam_step(const AdamTensor* tensors, const AdamArgs& a, cudaStream_t stream);
 cudaError_t launch_adam_moments(const AdamArgs& a, int64_t blocks, void* m_out, void* v_out,
                                 bool out_f32, cudaStream_t stream);
 

@@ -1598,14 +1598,14 @@ qlora_status qlora_adamw_step(const qlora_adamw_tensor* tensors, int count_,
     int64_t first = 0;
     int part = 0;
     for (int i = 0; i < count_; i += kAdamTensors) {
-      AdamTable table;
+      AdamTensor table[kAdamTensors];
       a.tensors = 0;
       int64_t blocks = 0;
       const int end = std::min(count_, i + kAdamTensors);
       for (int j = i; j < end; ++j) {
         const qlora_adamw_tensor& t = tensors[j];
         if (t.n == 0) continue;
-        AdamTensor& d = table.t[a.tensors++];
+        AdamTensor& d = table[a.tensors++];
         d.p = t.p;
         d.master = t.master;
         d.g = t.grad;

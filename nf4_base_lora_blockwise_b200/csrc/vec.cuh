@@ -116,4 +116,47 @@ __device__ __forceinline__ float stored<__nv_bfloat16>(float x) {
   return __bfloat162float(__float2bfloat16_rn(x));
 }
 
+// Two fp32 values in one register pair, with the rounding of the scalar operations.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pair(float a, float b) {
+  f2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ f2 pair_bits(uint32_t a, uint32_t b) {
+  f2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ float2 split(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ f2 both(float a) { return pair(a, a); }
+__device__ __forceinline__ float sum2(f2 v) {
+  const float2 t = split(v);
+  return t.x + t.y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(f2 v) {
+  const float2 t = split(v);
+  return floats_bf16x2(t.x, t.y);
+}
+__device__ __forceinline__ f2 unpack_bf16(uint32_t w) { return pair_bits(w << 16, w & 0xFFFF0000u); }
+
 }  // namespace qlora
