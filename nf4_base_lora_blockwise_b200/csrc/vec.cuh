@@ -1,7 +1,6 @@
 // vec.cuh -- vectors of VEC consecutive bf16 or fp32 elements between global memory and fp32
-// registers, for the elementwise and row-wise kernels.  VEC * sizeof(T) is one 16-byte access or
-// two (8 elements), one access of 4 or 8 bytes (2 elements) or a single element; pointers are
-// aligned to it.
+// registers, for the elementwise and row-wise kernels.  VEC * sizeof(T) is one access of up to 16
+// bytes, or two of 16 (8 fp32 elements); pointers are aligned to it.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -20,7 +19,7 @@ __device__ __forceinline__ uint32_t floats_bf16x2(float a, float b) {
 
 template <int VEC>
 __device__ __forceinline__ void load_vec(const __nv_bfloat16* p, float (&f)[VEC]) {
-  static_assert(VEC == 8 || VEC == 2 || VEC == 1, "vector width");
+  static_assert(VEC == 8 || VEC == 4 || VEC == 2 || VEC == 1, "vector width");
   if constexpr (VEC == 8) {
     const uint4 v = *reinterpret_cast<const uint4*>(p);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -30,6 +29,13 @@ __device__ __forceinline__ void load_vec(const __nv_bfloat16* p, float (&f)[VEC]
       f[2 * i] = t.x;
       f[2 * i + 1] = t.y;
     }
+  } else if constexpr (VEC == 4) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    const float2 a = bf16x2_floats(v.x), b = bf16x2_floats(v.y);
+    f[0] = a.x;
+    f[1] = a.y;
+    f[2] = b.x;
+    f[3] = b.y;
   } else if constexpr (VEC == 2) {
     const float2 t = bf16x2_floats(*reinterpret_cast<const uint32_t*>(p));
     f[0] = t.x;
@@ -41,10 +47,10 @@ __device__ __forceinline__ void load_vec(const __nv_bfloat16* p, float (&f)[VEC]
 
 template <int VEC>
 __device__ __forceinline__ void load_vec(const float* p, float (&f)[VEC]) {
-  static_assert(VEC == 8 || VEC == 2 || VEC == 1, "vector width");
-  if constexpr (VEC == 8) {
+  static_assert(VEC == 8 || VEC == 4 || VEC == 2 || VEC == 1, "vector width");
+  if constexpr (VEC >= 4) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < VEC / 4; ++i) {
       const float4 v = reinterpret_cast<const float4*>(p)[i];
       f[4 * i] = v.x;
       f[4 * i + 1] = v.y;
@@ -69,6 +75,8 @@ __device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&f)[VEC
     v.z = floats_bf16x2(f[4], f[5]);
     v.w = floats_bf16x2(f[6], f[7]);
     *reinterpret_cast<uint4*>(p) = v;
+  } else if constexpr (VEC == 4) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(floats_bf16x2(f[0], f[1]), floats_bf16x2(f[2], f[3]));
   } else if constexpr (VEC == 2) {
     *reinterpret_cast<uint32_t*>(p) = floats_bf16x2(f[0], f[1]);
   } else {
@@ -78,9 +86,9 @@ __device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&f)[VEC
 
 template <int VEC>
 __device__ __forceinline__ void store_vec(float* p, const float (&f)[VEC]) {
-  if constexpr (VEC == 8) {
+  if constexpr (VEC >= 4) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < VEC / 4; ++i)
       reinterpret_cast<float4*>(p)[i] =
           make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
   } else if constexpr (VEC == 2) {

@@ -47,7 +47,8 @@ def _rnd(*shape, dtype=BF16, seed=0):
 
 
 @pytest.mark.parametrize("hd,rd", [(128, 128), (128, 64), (64, 64), (80, 80), (80, 40), (96, 24),
-                                   (192, 128), (256, 256), (36, 36), (36, 18), (10, 6), (7, 2),
+                                   (192, 128), (256, 256), (36, 36), (36, 18), (72, 24), (40, 8),
+                                   (10, 6), (7, 2),
                                    (2, 2), (33, 32), (512, 510), (2048, 2048)])
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_head_layouts(hd, rd, interleaved):
