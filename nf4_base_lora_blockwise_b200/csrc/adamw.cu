@@ -68,23 +68,38 @@ __device__ __forceinline__ f2 decode2(const float* table, uint32_t word, int k, 
   const uint32_t a = (word >> (8 * k)) & 255u, b = (word >> (8 * k + 8)) & 255u;
   return mul2(pair(table[a], table[b]), scale);
 }
-// Codes of a magnitude x = |m| / scale or sqrt(v) / scale in [0, 1] that is not below the least
-// value; r: 16 random bits.  (A little past 1 the carry still stays within the top code; what a
-// NaN or infinity gives does not matter, its block's scale is not finite.)
+// Codes, in the top byte, of a magnitude x = |m| / scale or sqrt(v) / scale in [0, 1] that is not
+// below the least value; r: 32 random bits, m's 16 the low ones.  The fp32 bits with the code in
+// their top byte, less the grid's base, plus the random bits below the code: a byte permutation
+// places these and the base's byte.  (A little past 1 the carry still stays within the top code;
+// what a NaN or infinity gives does not matter, its block's scale is not finite.)
+static_assert((kMBase + 0x87u) % 256 == 0 && (kVBase + 0x0Fu) % 256 == 0, "the bases' bytes");
 __device__ __forceinline__ uint32_t encode_m(float x, uint32_t r) {
-  return (__float_as_uint(x) + (r << 4) - (kMBase << 20)) >> 20;
+  return (__float_as_uint(x) << 4) + __byte_perm(r, 0x87u, 0x4105);
 }
 __device__ __forceinline__ uint32_t encode_v(float x, uint32_t r) {
-  return (__float_as_uint(x) + (r << 3) - (kVBase << 19)) >> 19;
+  return (__float_as_uint(x) << 5) + __byte_perm(r, 0x0Fu, 0x4325);
 }
 // ... and of any x.
 __device__ __forceinline__ uint32_t encode_m_any(float x, uint32_t r) {
-  if (x < kMLeast) return __fmul_rn(static_cast<float>(r), kMLeast / 65536.f) < x ? 1u : 0u;
+  if (x < kMLeast)
+    return __fmul_rn(static_cast<float>(r & 0xFFFFu), kMLeast / 65536.f) < x ? 1u << 24 : 0u;
   return encode_m(x, r);
 }
 __device__ __forceinline__ uint32_t encode_v_any(float x, uint32_t r) {
-  if (x < kVLeast) return x > 0.f ? 1u : 0u;
+  if (x < kVLeast) return x > 0.f ? 1u << 24 : 0u;
   return encode_v(x, r);
+}
+// The top bytes of four words.
+__device__ __forceinline__ uint32_t top_bytes(const uint32_t (&u)[8], int k) {
+  return __byte_perm(__byte_perm(u[k], u[k + 1], 0x0073), __byte_perm(u[k + 2], u[k + 3], 0x0073),
+                     0x5410);
+}
+// The larger magnitude, NaN where one is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
 }
 
 // The tensor that block `b` of the launch belongs to.
@@ -361,21 +376,24 @@ __global__ void __launch_bounds__(kAdamThreads, 4)
       load_block(table.t[ti], a, b, lane, h);
     }
     if constexpr (BITS8) {
-      uint32_t am = 0, ar = 0;  // as bits: a NaN is the largest, and the block's scale
+      // The largest |m| and root: as bits a NaN is the largest of all, and the block's scale.
+      float tm = fabsf(m[0]), tr = root[0], lm = tm, lr_ = tr;  // ... and the least
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        am = max(am, __float_as_uint(m[k]) & 0x7FFFFFFFu);
-        ar = max(ar, __float_as_uint(root[k]) & 0x7FFFFFFFu);
+      for (int k = 1; k < 8; ++k) {
+        tm = max_nan(tm, fabsf(m[k]));
+        tr = max_nan(tr, root[k]);
+        lm = fminf(lm, fabsf(m[k]));
+        lr_ = fminf(lr_, root[k]);
       }
-      am = __reduce_max_sync(0xFFFFFFFFu, am);
-      ar = __reduce_max_sync(0xFFFFFFFFu, ar);
+      uint32_t am = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(tm));
+      uint32_t ar = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(tr));
       if (am < 0x00800000u) am = 0;  // below the normal numbers: a block of zeros
       if (ar < 0x00800000u) ar = 0;
       const float sm = __uint_as_float(am), sv = __uint_as_float(ar);
       const f2 im = both(am ? __fdiv_rn(1.f, sm) : 0.f), iv = both(ar ? __fdiv_rn(1.f, sv) : 0.f);
       const uint32_t lo = static_cast<uint32_t>(e0);
       const uint32_t hi = static_cast<uint32_t>(static_cast<uint64_t>(e0) >> 32) * 0x9E3779B1u;
-      uint32_t cm[2] = {0, 0}, cv[2] = {0, 0};
+      uint32_t um[8], uv[8];
       auto make = [&](auto em, auto ev) {
 #pragma unroll
         for (int k = 0; k < 8; k += 2) {
@@ -384,33 +402,19 @@ __global__ void __launch_bounds__(kAdamThreads, 4)
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             const uint32_t r = mix32(((lo + k + q) ^ hi) + word);
-            const uint32_t c = (em(q ? x.y : x.x, r & 0xFFFFu) & 127u) |
-                               ((__float_as_uint(m[k + q]) >> 24) & 128u);
-            const uint32_t d = ev(q ? y.y : y.x, r >> 16) & 255u;
-            if ((k + q) & 3) {
-              cm[k >> 2] |= c << (8 * ((k + q) & 3));
-              cv[k >> 2] |= d << (8 * ((k + q) & 3));
-            } else {
-              cm[k >> 2] = c;
-              cv[k >> 2] = d;
-            }
+            const uint32_t c = em(q ? x.y : x.x, r);
+            um[k + q] = (c & 0x7FFFFFFFu) | (__float_as_uint(m[k + q]) & 0x80000000u);
+            uv[k + q] = ev(q ? y.y : y.x, r);
           }
         }
       };
-      // The least of the block's |m| and roots, against the grids' least values.
-      float lm = fabsf(m[0]), lr_ = root[0];
-#pragma unroll
-      for (int k = 1; k < 8; ++k) {
-        lm = fminf(lm, fabsf(m[k]));
-        lr_ = fminf(lr_, root[k]);
-      }
       // (A little above, for the rounding of the quotients.)
       if (__any_sync(0xFFFFFFFFu, !(lm > 1.001f * kMLeast * sm && lr_ > 1.001f * kVLeast * sv)))
         make(encode_m_any, encode_v_any);
       else
         make(encode_m, encode_v);
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.m) + e0) = make_uint2(cm[0], cm[1]);
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v) + e0) = make_uint2(cv[0], cv[1]);
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.m) + e0) = make_uint2(top_bytes(um, 0), top_bytes(um, 4));
+      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v) + e0) = make_uint2(top_bytes(uv, 0), top_bytes(uv, 4));
       if (lane == 0) {
         a.m_scale[gb] = sm;
         a.v_scale[gb] = sv;
