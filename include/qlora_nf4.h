@@ -547,6 +547,12 @@ QLORA_API size_t qlora_noalloc_scratch_bytes(void);
  * context stays usable. */
 QLORA_API qlora_status qlora_selftest_bounded_wait(qlora_stream_t stream);
 
+/* Self-test of the AdamW step's square root: adds to the device counter *wrong the number of fp32
+ * numbers, of `count` with consecutive bits from `first` on, whose root is not the correctly
+ * rounded one.  It is meant for [1e-30, 1e30]. */
+QLORA_API qlora_status qlora_selftest_root(uint32_t first, uint32_t count, uint32_t* wrong,
+                                           qlora_stream_t stream);
+
 /* Synchronising: returns the device error word of the current device (0 = none; otherwise
  * a code naming the wait that ran out) and clears it. */
 QLORA_API qlora_status qlora_device_error(int* code);

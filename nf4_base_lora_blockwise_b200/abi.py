@@ -55,6 +55,7 @@ EXPORTS = (
     "qlora_set_side_overlap",
     "qlora_backward_side_sms",
     "qlora_selftest_bounded_wait",
+    "qlora_selftest_root",
 )
 
 STATUS = {
@@ -172,6 +173,7 @@ def _lib():
             "qlora_noalloc_scratch_bytes": (_SZ, []),
             "qlora_device_error": (_I, [ctypes.POINTER(ctypes.c_int)]),
             "qlora_selftest_bounded_wait": (_I, [_VP]),
+            "qlora_selftest_root": (_I, [ctypes.c_uint32, ctypes.c_uint32, _VP, _VP]),
             "qlora_grouped_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
             "qlora_swiglu_packed_fwd": (_I, [_VP, _VP, _I64, _I, _VP]),
             "qlora_swiglu_packed_bwd": (_I, [_VP, _VP, _VP, _I64, _I, _VP]),
@@ -483,6 +485,10 @@ def qlora_noalloc_scratch_bytes():
 
 def qlora_selftest_bounded_wait(stream):
     _check("qlora_selftest_bounded_wait", _lib().qlora_selftest_bounded_wait(stream))
+
+
+def qlora_selftest_root(first, count, wrong, stream):
+    _check("qlora_selftest_root", _lib().qlora_selftest_root(first, count, wrong, stream))
 
 
 def qlora_device_error():

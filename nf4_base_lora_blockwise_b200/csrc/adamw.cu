@@ -102,6 +102,25 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
+// Square roots of two numbers in [kRootLow, kRootHigh], correctly rounded: the approximate
+// reciprocal root r, s = v r, and Markstein's correction s + (v - s^2) r / 2 with a fused residual
+// ("IA-64 and Elementary Functions", square root), which leaves a relative 2^-45 before the last
+// rounding.  That this is the nearest for every mantissa and both parities of the exponent was
+// tested exhaustively (qlora_selftest_root); scaling by a power of 4 changes nothing.
+constexpr float kRootLow = 1e-30f, kRootHigh = 1e30f;
+__device__ __forceinline__ float rsqrt_approx(float x) {
+  float r;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ f2 root2(f2 v) {
+  const float2 x = split(v);
+  const f2 r = pair(rsqrt_approx(x.x), rsqrt_approx(x.y));
+  const f2 s = mul2(v, r);
+  const f2 e = fma2(mul2(s, both(-1.f)), s, v);
+  return fma2(e, mul2(r, both(0.5f)), s);
+}
+
 // The tensor that block `b` of the launch belongs to.
 template <int N>
 __device__ __forceinline__ int tensor_of(const AdamTable<N>& t, int n, uint32_t b) {
@@ -216,7 +235,7 @@ __global__ void __launch_bounds__(kAdamThreads)
 template <bool BITS8>
 struct Held {
   float p[8], g[8];
-  f2 m[BITS8 ? 1 : 4], v[BITS8 ? 1 : 4];
+  f2 m[BITS8 ? 1 : 4], v[BITS8 ? 1 : 4];  // 32 bits
   uint2 cm, cv;
   float sm, sv;
 };
@@ -294,7 +313,8 @@ __global__ void __launch_bounds__(kAdamThreads, 4)
     const int64_t e0 = gb * kAdamBlock + lane * 8;  // element of the list
     const float rate = lr * t.lr_scale;
     const f2 keep = both(1.f - rate * t.weight_decay), move = both(-rate * c1);
-    float m[8], root[8], p[8];
+    f2 m2[4], v2[4];
+    float vmax = 0.f, vmin = 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const f2 g = mul2(pair(h.g[2 * k], h.g[2 * k + 1]), fac);
@@ -307,22 +327,31 @@ __global__ void __launch_bounds__(kAdamThreads, 4)
         mk = h.m[k];
         vk = h.v[k];
       }
-      mk = add2(mul2(mk, both(a.b1)), mul2(g, both(a.one_b1)));
-      vk = add2(mul2(vk, both(a.b2)), mul2(mul2(g, g), both(a.one_b2)));
-      const float2 v = split(vk), mm = split(mk);
-      m[2 * k] = mm.x;
-      m[2 * k + 1] = mm.y;
-      root[2 * k] = sqrtf(v.x);
-      root[2 * k + 1] = sqrtf(v.y);
-      const float2 d = split(fma2(pair(root[2 * k], root[2 * k + 1]), c2, eps));
+      m2[k] = add2(mul2(mk, both(a.b1)), mul2(g, both(a.one_b1)));
+      v2[k] = add2(mul2(vk, both(a.b2)), mul2(mul2(g, g), both(a.one_b2)));
+      const float2 v = split(v2[k]);
+      vmax = k == 0 ? max_nan(v.x, v.y) : max_nan(vmax, max_nan(v.x, v.y));
+      vmin = k == 0 ? fminf(v.x, v.y) : fminf(vmin, fminf(v.x, v.y));
+    }
+    f2 root[4];
+    if (__all_sync(0xFFFFFFFFu, vmin >= kRootLow && vmax <= kRootHigh)) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) root[k] = root2(v2[k]);
+    } else {  // zeros and other extremes
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 v = split(v2[k]);
+        root[k] = pair(sqrtf(v.x), sqrtf(v.y));
+      }
+    }
+    float p[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 d = split(fma2(root[k], c2, eps)), mm = split(m2[k]);
       const f2 u = pair(__fdividef(mm.x, d.x), __fdividef(mm.y, d.y));
       const float2 q = split(fma2(u, move, mul2(pair(h.p[2 * k], h.p[2 * k + 1]), keep)));
       p[2 * k] = q.x;
       p[2 * k + 1] = q.y;
-      if constexpr (!BITS8) {
-        h.m[k] = mk;
-        h.v[k] = vk;
-      }
     }
     // Parameters.
     const bool whole = i + 8 <= t.n;
@@ -364,7 +393,7 @@ __global__ void __launch_bounds__(kAdamThreads, 4)
       for (int s = 0; s < 2; ++s) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const float2 x = split(s == 0 ? h.m[k] : h.v[k]);
+          const float2 x = split(s == 0 ? m2[k] : v2[k]);
           f[2 * k] = x.x;
           f[2 * k + 1] = x.y;
         }
@@ -376,17 +405,19 @@ __global__ void __launch_bounds__(kAdamThreads, 4)
       load_block(table.t[ti], a, b, lane, h);
     }
     if constexpr (BITS8) {
-      // The largest |m| and root: as bits a NaN is the largest of all, and the block's scale.
-      float tm = fabsf(m[0]), tr = root[0], lm = tm, lr_ = tr;  // ... and the least
+      // The largest |m| and v of the block, as bits, of which a NaN is the largest of all.
+      float tm = 0.f, lm = 0.f;
 #pragma unroll
-      for (int k = 1; k < 8; ++k) {
-        tm = max_nan(tm, fabsf(m[k]));
-        tr = max_nan(tr, root[k]);
-        lm = fminf(lm, fabsf(m[k]));
-        lr_ = fminf(lr_, root[k]);
+      for (int k = 0; k < 4; ++k) {
+        const float2 x = split(m2[k]);
+        const float hi2 = max_nan(fabsf(x.x), fabsf(x.y)), lo2 = fminf(fabsf(x.x), fabsf(x.y));
+        tm = k == 0 ? hi2 : max_nan(tm, hi2);
+        lm = k == 0 ? lo2 : fminf(lm, lo2);
       }
       uint32_t am = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(tm));
-      uint32_t ar = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(tr));
+      // (The root rounds monotonically: the largest root is the largest v's.)
+      uint32_t ar = __float_as_uint(
+          sqrtf(__uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(vmax)))));
       if (am < 0x00800000u) am = 0;  // below the normal numbers: a block of zeros
       if (ar < 0x00800000u) ar = 0;
       const float sm = __uint_as_float(am), sv = __uint_as_float(ar);
@@ -397,19 +428,22 @@ __global__ void __launch_bounds__(kAdamThreads, 4)
       auto make = [&](auto em, auto ev) {
 #pragma unroll
         for (int k = 0; k < 8; k += 2) {
-          const float2 x = split(mul2(pair(fabsf(m[k]), fabsf(m[k + 1])), im));
-          const float2 y = split(mul2(pair(root[k], root[k + 1]), iv));
+          const float2 s = split(m2[k / 2]);
+          const float2 x = split(mul2(pair(fabsf(s.x), fabsf(s.y)), im));
+          const float2 y = split(mul2(root[k / 2], iv));
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             const uint32_t r = mix32(((lo + k + q) ^ hi) + word);
             const uint32_t c = em(q ? x.y : x.x, r);
-            um[k + q] = (c & 0x7FFFFFFFu) | (__float_as_uint(m[k + q]) & 0x80000000u);
+            um[k + q] =
+                (c & 0x7FFFFFFFu) | (__float_as_uint(q ? s.y : s.x) & 0x80000000u);
             uv[k + q] = ev(q ? y.y : y.x, r);
           }
         }
       };
       // (A little above, for the rounding of the quotients.)
-      if (__any_sync(0xFFFFFFFFu, !(lm > 1.001f * kMLeast * sm && lr_ > 1.001f * kVLeast * sv)))
+      if (__any_sync(0xFFFFFFFFu, !(lm > 1.001f * kMLeast * sm &&
+                                      vmin > 1.002f * (kVLeast * sv) * (kVLeast * sv))))
         make(encode_m_any, encode_v_any);
       else
         make(encode_m, encode_v);
@@ -428,6 +462,19 @@ __global__ void __launch_bounds__(kAdamThreads, 4)
       st->ticket = 0;
     }
   }
+}
+
+// Counts the numbers first, first + 1, ... (as bits) whose root2 is not sqrtf's.
+__global__ void __launch_bounds__(kAdamThreads)
+    root_selftest_kernel(uint32_t first, uint32_t count, uint32_t* wrong) {
+  uint32_t bad = 0;
+  for (uint32_t i = blockIdx.x * kAdamThreads + threadIdx.x; i < count;
+       i += gridDim.x * kAdamThreads) {
+    const float x = __uint_as_float(first + i);
+    const float2 r = split(root2(both(x)));
+    bad += r.x != sqrtf(x) || r.y != r.x;
+  }
+  if (bad) atomicAdd(wrong, bad);
 }
 
 // The values that 8-bit moments stand for.
@@ -519,6 +566,12 @@ cudaError_t launch_adam_moments(const AdamArgs& a, int64_t blocks, void* m_out, 
   return launch_pdl(adam_moments_kernel<__nv_bfloat16>, grid, dim3(kAdamThreads), 0, stream, 1, m,
                     v, a.m_scale, a.v_scale, vectors, static_cast<__nv_bfloat16*>(m_out),
                     static_cast<__nv_bfloat16*>(v_out));
+}
+
+cudaError_t launch_root_selftest(uint32_t first, uint32_t count, uint32_t* wrong,
+                                 cudaStream_t stream) {
+  root_selftest_kernel<<<148 * 8, kAdamThreads, 0, stream>>>(first, count, wrong);
+  return cudaGetLastError();
 }
 
 }  // namespace qlora

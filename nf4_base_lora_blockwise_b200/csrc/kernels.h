@@ -491,6 +491,8 @@ int adam_norm_ctas(uint32_t blocks);
 // tensors: a.tensors of them.
 cudaError_t launch_adam_norm(const AdamTensor* tensors, const AdamArgs& a, cudaStream_t stream);
 cudaError_t launch_adam_step(const AdamTensor* tensors, const AdamArgs& a, cudaStream_t stream);
+cudaError_t launch_root_selftest(uint32_t first, uint32_t count, uint32_t* wrong,
+                                 cudaStream_t stream);
 cudaError_t launch_adam_moments(const AdamArgs& a, int64_t blocks, void* m_out, void* v_out,
                                 bool out_f32, cudaStream_t stream);
 

@@ -1294,6 +1294,18 @@ qlora_status qlora_swiglu_packed_bwd(const void* gu, const void* da, void* dgu, 
   return st;
 }
 
+qlora_status qlora_selftest_root(uint32_t first, uint32_t count_, uint32_t* wrong,
+                                 qlora_stream_t stream) {
+  if (!wrong) return QLORA_ERR_NULL;
+  if (!aligned16(wrong)) return QLORA_ERR_ALIGN;
+  int dev;
+  qlora_status st = current_device(&dev);
+  if (st != QLORA_OK) return st;
+  st = cuda_status(launch_root_selftest(first, count_, wrong, static_cast<cudaStream_t>(stream)));
+  if (st == QLORA_OK) count(1);
+  return st;
+}
+
 static bool finite_f(double x) { return std::isfinite(x); }
 
 qlora_status qlora_residual_norm_fwd(const void* h, const void* y, const void* w_pre,

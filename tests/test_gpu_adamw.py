@@ -295,6 +295,20 @@ def test_learning_rate_on_the_device_and_assigned():
     assert float(a.lr) == 0.0 and b.lr == 0.0
 
 
+def test_square_roots_are_the_nearest():
+    """Every mantissa under both parities of the exponent, at 1, and near both ends of the range."""
+    from nf4_base_lora_blockwise_b200 import abi
+    wrong = torch.zeros(4, dtype=torch.int32, device="cuda")
+    for x in (1.0, 1.2e-30, 2.0 ** 90):
+        first = int(np.float32(x).view(np.uint32))
+        first = first if x == 1.0 else first & 0xFF800000
+        if x == 1.2e-30:
+            first += 1 << 23              # a whole binade above the low end
+        abi.qlora_selftest_root(first, 1 << 24, wrong.data_ptr(),
+                                torch.cuda.current_stream().cuda_stream)
+    assert torch.count_nonzero(wrong) == 0
+
+
 def test_refusals():
     z = lambda n=8, dtype=F32: torch.zeros(n, dtype=dtype, device="cuda")  # noqa: E731
     p = z()
