@@ -1306,6 +1306,8 @@ qlora_status qlora_selftest_root(uint32_t first, uint32_t count_, uint32_t* wron
   return st;
 }
 
+static bool norm_width(int D) { return D >= 1 && D <= kNormMaxD && (D % 8 == 0 || D <= kNormMaxD - 8); }
+
 static bool finite_f(double x) { return std::isfinite(x); }
 
 qlora_status qlora_residual_norm_fwd(const void* h, const void* y, const void* w_pre,
@@ -1315,7 +1317,7 @@ qlora_status qlora_residual_norm_fwd(const void* h, const void* y, const void* w
                                      float* rstd_pre, float* rstd_post, qlora_stream_t stream) {
   if (!h || (!y && !w_pre) || (w_pre && !n) || (y && !h_out)) return QLORA_ERR_NULL;
   if (gate_kind != QLORA_GATE_NONE && !gate) return QLORA_ERR_NULL;
-  if (M < 0 || D < 1 || D > kNormMaxD || gate_kind < QLORA_GATE_NONE ||
+  if (M < 0 || !norm_width(D) || gate_kind < QLORA_GATE_NONE ||
       gate_kind > QLORA_GATE_FULL || (types & ~7))
     return QLORA_ERR_SHAPE;
   // What nothing would write or read is a mistake of the caller's.
@@ -1358,7 +1360,7 @@ qlora_status qlora_residual_norm_fwd(const void* h, const void* y, const void* w
 }
 
 size_t qlora_residual_norm_workspace_bytes(int64_t M, int D) {
-  if (M < 1 || D < 1 || D > kNormMaxD) return 0;
+  if (M < 1 || !norm_width(D)) return 0;
   return align256(residual_norm_part_bytes(M, D));
 }
 
@@ -1375,7 +1377,7 @@ qlora_status qlora_residual_norm_bwd(const void* dn, const void* dh_out, const v
   if (!w_post && dw_post) return QLORA_ERR_NULL;
   if (gate_kind != QLORA_GATE_NONE && (!gate || !dy)) return QLORA_ERR_NULL;
   if (dgate && !y) return QLORA_ERR_NULL;
-  if (M < 0 || D < 1 || D > kNormMaxD || gate_kind < QLORA_GATE_NONE ||
+  if (M < 0 || !norm_width(D) || gate_kind < QLORA_GATE_NONE ||
       gate_kind > QLORA_GATE_FULL || (types & ~7) ||
       (gate_kind == QLORA_GATE_NONE && (gate || dgate)))
     return QLORA_ERR_SHAPE;

@@ -17,9 +17,8 @@
 // slot for the last time, so a row is on its way while the one before is worked on, without a
 // barrier or a second stage.
 //
-// Rows of D % 8 != 0 start anywhere in a 16-byte granule: threads still copy and store whole
-// granules and shift them by the row's offset with their neighbours' through shuffles, instead of
-// 2-byte accesses.
+// Rows of D % 8 != 0 start anywhere in a 16-byte granule: threads copy and store the granules as
+// they lie, and address what belongs to columns by the row's offset (residual_norm.cuh).
 #include "residual_norm.cuh"
 
 namespace qlora {
@@ -45,7 +44,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   extern __shared__ __align__(16) unsigned char smem_raw[];
   __shared__ __align__(16) float buf[4][kSumBuf];
   const uint32_t smem = smem_u32(smem_raw);
-  const Lane<NV> l = lane_of<NV, T>(ring, smem, a.D);
+  const Lane<NV> l = lane_of<NV, T, ALIGNED>(ring, smem, a.D);
   pdl_wait();  // the previous kernel's outputs are complete
   pdl_trigger();
   const float inv_d = 1.f / static_cast<float>(a.D);
@@ -68,12 +67,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   if constexpr (ALIGNED) clear_slots<NV, T>(ring, l, r);
   // Two copy groups a row: y, then h and a whole gate.
   auto start_y = [&](const RowAt& q) {
-    if (a.y) issue<2, NV, T, ALIGNED, 0, S::Y>(a.y, l, q);
+    if (a.y) issue<2, NV, T, ALIGNED, S::Y>(a.y, l, q);
     commit_copies();
   };
   auto start_h = [&](const RowAt& q) {
-    issue<RB, NV, T, ALIGNED, 1, S::H>(a.h, l, q);
-    if constexpr (GF) issue_gate<NV, T, ALIGNED, 2, S::GATE>(a.gate, ring, l, q);
+    issue<RB, NV, T, ALIGNED, S::H>(a.h, l, q);
+    if constexpr (GF) issue_gate<NV, T, ALIGNED, S::GATE>(a.gate, ring, l, q);
     commit_copies();
   };
   start_y(r);
@@ -100,7 +99,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       f2 ss = both(0.f);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        fetch<2, NV, T, ALIGNED, 0, S::Y>(a.y, l, r, j, y[j]);
+        fetch<2, NV, T, ALIGNED, S::Y>(a.y, l, r, j, y[j]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) ss = fma2(y[j][k], y[j][k], ss);
       }
@@ -119,17 +118,17 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       for (int j = 0; j < NV; ++j) {
         if (wide) {
           f2 v[4];
-          weights8<1, WS, ALIGNED>(w, ring, l, j, v);
+          weights8<1, WS, ALIGNED>(w, ring, l, smem_raw, r, j, v);
 #pragma unroll
           for (int k = 0; k < 4; ++k) y[j][k] = mul2(y[j][k], v[k]);
         }
         if constexpr (GF) {
           f2 g[4];
-          fetch_gate<NV, T, ALIGNED, 2, S::GATE>(a.gate, ring, l, r, j, g);
+          fetch_gate<NV, T, ALIGNED, S::GATE>(a.gate, ring, l, r, j, g);
 #pragma unroll
           for (int k = 0; k < 4; ++k) y[j][k] = mul2(y[j][k], g[k]);
         }
-        fetch<RB, NV, T, ALIGNED, 1, S::H>(a.h, l, r, j, h[j]);
+        fetch<RB, NV, T, ALIGNED, S::H>(a.h, l, r, j, h[j]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           h[j][k] = fma2(y[j][k], sc, mul2(h[j][k], res));
@@ -141,7 +140,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       start_y(next);
       wait_copies<1>();
 #pragma unroll
-      for (int j = 0; j < NV; ++j) fetch<RB, NV, T, ALIGNED, 1, S::H>(a.h, l, r, j, h[j]);
+      for (int j = 0; j < NV; ++j) fetch<RB, NV, T, ALIGNED, S::H>(a.h, l, r, j, h[j]);
     }
     start_h(next);
     if (a.w_pre) {
@@ -158,7 +157,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         f2 v[4];
-        weights8<0, WS, ALIGNED>(w, ring, l, j, v);
+        weights8<0, WS, ALIGNED>(w, ring, l, smem_raw, r, j, v);
 #pragma unroll
         for (int k = 0; k < 4; ++k) h[j][k] = mul2(mul2(h[j][k], rr), v[k]);
         put<__nv_bfloat16, ALIGNED>(a.n, r, l.c[j], h[j]);
@@ -172,13 +171,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 }
 
 template <typename R, bool ALIGNED>
-cudaError_t launch_fwd(const ResidualNormFwd& a, const RowShape& s, cudaStream_t st) {
+cudaError_t launch_fwd(const ResidualNormFwd& a, RowShape s, cudaStream_t st) {
   Ring ring = {};
   bool ws;
   const bool weights = a.w_pre || a.w_post || a.gate_kind == kGateChannel;
   const bool gf = a.gate_kind == kGateFull;
-  const int smem = plan_ring(a.M, a.D, 3, FwdSlots<R, 2>::GATE, gf, a.gate_f32, weights, s, &ring,
-                             &ws);
+  const int smem = plan_ring(a.M, a.D, FwdSlots<R, 2>::GATE, gf, a.gate_f32, weights, false, s,
+                             &ring, &ws);
   if (gf)
     return ws ? launch_rows(residual_norm_fwd_kernel<R, ALIGNED, true, true>, s, a, ring, smem, st)
               : launch_rows(residual_norm_fwd_kernel<R, ALIGNED, false, true>, s, a, ring, smem,

@@ -18,14 +18,19 @@ namespace {
 // Row streams: [M, D] tensors read row by row.  Every thread has `slots` 16-byte slots in shared
 // memory, [slot][T threads] (a copy whose lanes do not write one contiguous piece of shared memory
 // measured a third slower); a stream's, and the T that a CTA has room for, are given at compile
-// time, so that an access is one register and a constant.  Rows that start inside a
-// granule need the granule after a warp's last: `extra`, one for each stream, vector and warp.
+// time, so that an access is one register and a constant.
+//
+// ALIGNED: D % 8 == 0, a vector is columns 8 v .. 8 v + 7.  Otherwise a row starts `shift` elements
+// inside a granule of 8, and vector v is the granule that starts 8 v elements after the row's
+// first one: columns 8 v - shift .. 8 v - shift + 7, where there are such columns.  All streams
+// and outputs share that, so whole granules are read and stored as they lie, but for a row's
+// ends; only what belongs to columns (weights, column sums) is addressed by column.
 // ---------------------------------------------------------------------------------------------
 struct Ring {
   int slots;       // of a thread
-  int extra;       // byte of the extra granules, [stream][nv][warp]
   int weights;     // byte of the combined weights' [2][weights_ld] fp32
-  int weights_ld;  // D rounded up to 8, and 8 zeros
+  int weights_ld;  // D rounded up to 8, and 8 zeros; or skewed_size(D)
+  int sums;        // byte of the column sums' [group][2][weights_ld] fp32, or -1: in `part`
   int gate_f32;    // a whole gate's type
   int gate_direct; // a whole gate that does not fit: read from global memory where it is used
 };
@@ -74,25 +79,33 @@ __device__ __forceinline__ uint4 ldg16(const void* p, int64_t e, int64_t total) 
   return ldg16_tail<ESIZE>(q, total - e);
 }
 
+// Rows that are not ALIGNED address fp32 arrays over columns -8 .. (D up to 8) + 15 in shared memory,
+// with a gap after every 8: neighbouring vectors lie 9 words apart and meet different banks.
+__host__ __device__ constexpr int skewed_size(int D) { return ((D + 7) / 8 + 3) * 9; }
+__device__ __forceinline__ int skewed(int c) { return (c + 8) + ((c + 8) >> 3); }
+
 template <int NV>
 struct Lane {
   uint32_t slots;  // shared address of the thread's first slot
-  uint32_t extra;  // of its warp's first extra granule
-  uint32_t w[NV];  // of the combined weights of its columns
-  int c[NV];       // first column of its vectors
+  uint32_t w[NV];  // ALIGNED: of the combined weights of its columns; else vector v's skewed index
+  int c[NV];       // 8 v
 };
-template <int NV, int T>
+template <int NV, int T, bool ALIGNED>
 __device__ __forceinline__ Lane<NV> lane_of(const Ring& ring, uint32_t smem, int D) {
   const int tid = threadIdx.y * blockDim.x + threadIdx.x;
   Lane<NV> l;
   l.slots = smem + tid * 16;
-  l.extra = smem + ring.extra + (tid >> 5) * 16;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     l.c[j] = (j * blockDim.x + threadIdx.x) * 8;
-    // Past the row's end: the zeros behind the weights.
-    const int at = l.c[j] < D ? l.c[j] : ring.weights_ld - 8;
-    l.w[j] = smem + ring.weights + at * 4;
+    if constexpr (ALIGNED) {
+      // Past the row's end: the zeros behind the weights.
+      const int at = l.c[j] < D ? l.c[j] : ring.weights_ld - 8;
+      l.w[j] = smem + ring.weights + at * 4;
+    } else {
+      const int last = (D + 7) / 8 * 8 + 8;  // its columns are past the end for every shift
+      l.w[j] = (l.c[j] < last ? l.c[j] : last) / 8 * 9 + 9;
+    }
   }
   return l;
 }
@@ -107,8 +120,8 @@ __device__ __forceinline__ void clear_slots(const Ring& ring, const Lane<NV>& l,
                  : "memory");
 }
 
-// Starts the copies of row r's granules of one stream (its number and first slot: STREAM, SLOT).
-template <int ESIZE, int NV, int T, bool ALIGNED, int STREAM, int SLOT>
+// Starts the copies of row r's granules of one stream, whose first slot is SLOT.
+template <int ESIZE, int NV, int T, bool ALIGNED, int SLOT>
 __device__ __forceinline__ void issue(const void* p, const Lane<NV>& l, const RowAt& r) {
   if (!r.row) return;
   constexpr int N = 16 / ESIZE;  // elements of a granule
@@ -124,85 +137,57 @@ __device__ __forceinline__ void issue(const void* p, const Lane<NV>& l, const Ro
       }
     }
   } else {
-    const int shift = static_cast<int>(r.at & (N - 1));
+    const int shift = static_cast<int>(r.at & 7);
     const int64_t a = r.at - shift;
     const char* base = static_cast<const char*>(p);
-    auto start = [&](uint32_t dst, int first) {  // the granule `first` elements after the row's
-      if (first >= r.D + shift) return;
-      const int64_t e = a + first;
-      const int bytes = e + N > r.total ? static_cast<int>(r.total - e) * ESIZE : 16;
-      copy16(dst, base + e * ESIZE, bytes);
-    };
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
 #pragma unroll
-      for (int g = 0; g < G; ++g) start(l.slots + (SLOT + j * G + g) * (T * 16), l.c[j] + g * N);
-      if ((threadIdx.x & 31) == 31) start(l.extra + (STREAM * NV + j) * (T / 32 * 16), l.c[j] + 8);
+      for (int g = 0; g < G; ++g) {
+        const int first = l.c[j] + g * N;
+        if (first >= r.D + shift) continue;
+        const int64_t e = a + first;
+        const int bytes = e + N > r.total ? static_cast<int>(r.total - e) * ESIZE : 16;
+        copy16(l.slots + (SLOT + j * G + g) * (T * 16), base + e * ESIZE, bytes);
+      }
     }
   }
 }
 
-// 8 columns of row r, j-th vector of the thread, as fp32 pairs; columns outside the row read 0.
+// The j-th vector of the thread as fp32 pairs; what lies outside the row reads 0.
 // DIRECT: from global memory.
-template <int ESIZE, int NV, int T, bool ALIGNED, int STREAM, int SLOT, bool DIRECT = false>
+template <int ESIZE, int NV, int T, bool ALIGNED, int SLOT, bool DIRECT = false>
 __device__ __forceinline__ void fetch(const void* p, const Lane<NV>& l, const RowAt& r, int j,
                                       f2 (&f)[4]) {
   constexpr int N = 16 / ESIZE;
   constexpr int G = 8 / N;
   const int c = l.c[j];
-  const int shift = ALIGNED ? 0 : static_cast<int>(r.at & (N - 1));
-  auto granule = [&](uint32_t src, int first) {
-    if constexpr (!DIRECT) return lds16(src);
-    return r.row && first < r.D + shift ? ldg16<ESIZE>(p, r.at - shift + first, r.total)
-                                        : make_uint4(0, 0, 0, 0);
-  };
-  uint32_t w[4 * G + 4];
+  const int shift = ALIGNED ? 0 : static_cast<int>(r.at & 7);
+  uint32_t w[4 * G];
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    const uint4 q = granule(l.slots + (SLOT + j * G + g) * (T * 16), c + g * N);
+    uint4 q;
+    if constexpr (DIRECT)
+      q = r.row && c + g * N < r.D + shift ? ldg16<ESIZE>(p, r.at - shift + c + g * N, r.total)
+                                           : make_uint4(0, 0, 0, 0);
+    else
+      q = lds16(l.slots + (SLOT + j * G + g) * (T * 16));
     w[4 * g] = q.x;
     w[4 * g + 1] = q.y;
     w[4 * g + 2] = q.z;
     w[4 * g + 3] = q.w;
   }
   if constexpr (!ALIGNED) {
-    // The next thread's first granule, then the window moves `shift` elements up.
-    uint32_t n[4];
+    // Before the row's start, past its end or without a row lies another row's, or nothing.
+    const int first = shift - c, end = r.row ? r.D + shift - c : 0;
+    if (first > 0 || end < 8) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) n[k] = __shfl_down_sync(0xFFFFFFFFu, w[k], 1);
-    if ((threadIdx.x & 31) == 31) {
-      const uint4 q = granule(l.extra + (STREAM * NV + j) * (T / 32 * 16), c + 8);
-      n[0] = q.x;
-      n[1] = q.y;
-      n[2] = q.z;
-      n[3] = q.w;
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) w[4 * G + k] = n[k];
-    const int words = ESIZE == 4 ? shift : shift >> 1;
-    if (words & 2) {
-#pragma unroll
-      for (int k = 0; k + 2 < 4 * G + 4; ++k) w[k] = w[k + 2];
-    }
-    if (words & 1) {
-#pragma unroll
-      for (int k = 0; k + 1 < 4 * G + 4; ++k) w[k] = w[k + 1];
-    }
-    if (ESIZE == 2 && (shift & 1)) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], 16);
-    }
-    // What lies past the row's end is the next row's, or left from another row.
-    const int left = r.row ? r.D - c : 0;
-    if (left < 8) {
-#pragma unroll
-      for (int k = 0; k < 4 * G; ++k) {
-        if constexpr (ESIZE == 4) {
-          if (k >= left) w[k] = 0;
-        } else {
-          if (2 * k >= left) w[k] = 0;
-          if (2 * k + 1 == left) w[k] &= 0xFFFFu;
-        }
+      for (int k = 0; k < 8; ++k) {
+        if (k >= first && k < end) continue;
+        if constexpr (ESIZE == 4)
+          w[k] = 0;
+        else
+          w[k / 2] &= k % 2 ? 0xFFFFu : 0xFFFF0000u;
       }
     }
   }
@@ -216,32 +201,31 @@ __device__ __forceinline__ void fetch(const void* p, const Lane<NV>& l, const Ro
 }
 
 // A whole gate, of a type known at run time.
-template <int NV, int T, bool ALIGNED, int STREAM, int SLOT>
+template <int NV, int T, bool ALIGNED, int SLOT>
 __device__ __forceinline__ void issue_gate(const void* p, const Ring& ring, const Lane<NV>& l,
                                            const RowAt& r) {
   if (ring.gate_direct) return;
   if (ring.gate_f32)
-    issue<4, NV, T, ALIGNED, STREAM, SLOT>(p, l, r);
+    issue<4, NV, T, ALIGNED, SLOT>(p, l, r);
   else
-    issue<2, NV, T, ALIGNED, STREAM, SLOT>(p, l, r);
+    issue<2, NV, T, ALIGNED, SLOT>(p, l, r);
 }
-template <int NV, int T, bool ALIGNED, int STREAM, int SLOT>
+template <int NV, int T, bool ALIGNED, int SLOT>
 __device__ __forceinline__ void fetch_gate(const void* p, const Ring& ring, const Lane<NV>& l,
                                            const RowAt& r, int j, f2 (&f)[4]) {
   if (ring.gate_direct) {
     if (ring.gate_f32)
-      fetch<4, NV, T, ALIGNED, STREAM, SLOT, true>(p, l, r, j, f);
+      fetch<4, NV, T, ALIGNED, SLOT, true>(p, l, r, j, f);
     else
-      fetch<2, NV, T, ALIGNED, STREAM, SLOT, true>(p, l, r, j, f);
+      fetch<2, NV, T, ALIGNED, SLOT, true>(p, l, r, j, f);
   } else if (ring.gate_f32) {
-    fetch<4, NV, T, ALIGNED, STREAM, SLOT>(p, l, r, j, f);
+    fetch<4, NV, T, ALIGNED, SLOT>(p, l, r, j, f);
   } else {
-    fetch<2, NV, T, ALIGNED, STREAM, SLOT>(p, l, r, j, f);
+    fetch<2, NV, T, ALIGNED, SLOT>(p, l, r, j, f);
   }
 }
 
-// Stores 8 columns of row r (columns outside the row are left alone).  All threads of the warp
-// call it together.
+// Stores the vector whose l.c[j] is c; what lies outside the row is left alone.
 template <typename T, bool ALIGNED>
 __device__ __forceinline__ void put(T* p, const RowAt& r, int c, const f2 (&f2s)[4]) {
   float f[8];
@@ -254,84 +238,18 @@ __device__ __forceinline__ void put(T* p, const RowAt& r, int c, const f2 (&f2s)
   if constexpr (ALIGNED) {
     if (r.row && c < r.D) store_vec<8>(p + r.at + c, f);
   } else {
-    constexpr int N = 16 / static_cast<int>(sizeof(T));
-    const int shift = static_cast<int>(r.at & (N - 1));
-    const int lane = threadIdx.x & 31;
-    // e[k]: the element at a + 8 v + k, a the row's first granule; its column is c - shift + k.
-    float e[8];
-    if constexpr (sizeof(T) == 4) {
-      float w[11];
-#pragma unroll
-      for (int k = 0; k < 3; ++k) w[k] = __shfl_up_sync(0xFFFFFFFFu, f[5 + k], 1);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) w[3 + k] = f[k];
-      // window from 3 - shift on
-      const int t = 3 - shift;
-      if (t & 2) {
-#pragma unroll
-        for (int k = 0; k + 2 < 11; ++k) w[k] = w[k + 2];
-      }
-      if (t & 1) {
-#pragma unroll
-        for (int k = 0; k + 1 < 11; ++k) w[k] = w[k + 1];
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) e[k] = w[k];
-    } else {
-      // halfwords: the previous thread's 8, then this one's; window from 8 - shift on
-      uint32_t w[9];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) w[4 + k] = floats_bf16x2(f[2 * k], f[2 * k + 1]);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) w[k] = __shfl_up_sync(0xFFFFFFFFu, w[4 + k], 1);
-      w[8] = 0;
-      const int t = 8 - shift, h = t >> 1;
-      if (h & 4) {
-#pragma unroll
-        for (int k = 0; k < 5; ++k) w[k] = w[k + 4];
-      }
-      if (h & 2) {
-#pragma unroll
-        for (int k = 0; k < 6; ++k) w[k] = w[k + 2];
-      }
-      if (h & 1) {
-#pragma unroll
-        for (int k = 0; k < 6; ++k) w[k] = w[k + 1];
-      }
-      if (t & 1) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], 16);
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 q = bf16x2_floats(w[k]);
-        e[2 * k] = q.x;
-        e[2 * k + 1] = q.y;
-      }
-    }
     if (!r.row) return;
+    const int shift = static_cast<int>(r.at & 7);
     T* q = p + (r.at - shift) + c;
-    const int c0 = c - shift;
-    if ((lane > 0 || shift == 0) && c0 >= 0 && c0 + 8 <= r.D) {
-      store_vec<8>(q, e);
-    } else {
-      // The row's ends, and the first lane's granule, of which the warp before has the start.
+    const int first = shift - c, end = r.D + shift - c;
+    if (first <= 0 && end >= 8) {
+      store_vec<8>(q, f);
+    } else if (end > 0) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const int col = c0 + k;
-        if (col >= 0 && col < r.D && (lane > 0 || k >= shift)) {
-          const float one[1] = {e[k]};
-          store_vec<1>(q + k, one);
-        }
-      }
-    }
-    if (lane == 31) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {  // the last `shift` columns of f start the next granule
-        if (k >= 8 - shift && c + k < r.D) {
-          const float one[1] = {f[k]};
-          store_vec<1>(q + shift + k, one);
-        }
+        if (k < first || k >= end) continue;
+        const float one[1] = {f[k]};
+        store_vec<1>(q + k, one);
       }
     }
   }
@@ -348,38 +266,29 @@ struct Weights {
   float offset;
   int D;
 };
-__device__ __noinline__ void columns_tail(const void* p, bool f32, int c, int D, float* f) {
-  for (int k = 0; k < 8; ++k) f[k] = c + k < D ? load_either1(p, f32, c + k) : 0.f;
+template <int WHICH>
+__device__ __forceinline__ float combine1(const Weights& w, int c) {
+  const void* p = WHICH == 0 ? w.w_pre : w.w_post;
+  float f = p ? load_either1(p, w.weight_f32, c) + w.offset : 1.f;
+  if (WHICH == 1 && w.gate) f *= load_either1(w.gate, w.gate_f32, c);
+  return f;
 }
-template <bool ALIGNED>
-__device__ __forceinline__ void columns8(const void* p, bool f32, int c, int D, float (&f)[8]) {
-  if (ALIGNED || c + 8 <= D) {
-    load_either<8>(p, f32, c, f);
-  } else {
-    float t[8];
-    columns_tail(p, f32, c, D, t);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) f[k] = t[k];
-  }
-}
-template <int WHICH, bool ALIGNED>
+template <int WHICH>
 __device__ __forceinline__ void combine8(const Weights& w, int c, float (&f)[8]) {
   const void* p = WHICH == 0 ? w.w_pre : w.w_post;
   if (p) {
-    columns8<ALIGNED>(p, w.weight_f32, c, w.D, f);
+    load_either<8>(p, w.weight_f32, c, f);
 #pragma unroll
     for (int k = 0; k < 8; ++k) f[k] += w.offset;
   } else {
 #pragma unroll
     for (int k = 0; k < 8; ++k) f[k] = 1.f;
   }
-  if (WHICH == 1) {
-    if (w.gate) {
-      float g[8];
-      columns8<ALIGNED>(w.gate, w.gate_f32, c, w.D, g);
+  if (WHICH == 1 && w.gate) {
+    float g[8];
+    load_either<8>(w.gate, w.gate_f32, c, g);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f[k] *= g[k];
-    }
+    for (int k = 0; k < 8; ++k) f[k] *= g[k];
   }
 }
 // Fills the CTA's shared copy (a barrier follows before the first use).
@@ -388,22 +297,40 @@ __device__ __forceinline__ void stage_weights(const Weights& w, const Ring& ring
                                               unsigned char* smem, bool second) {
   float* d = reinterpret_cast<float*>(smem + ring.weights);
   const int tid = threadIdx.y * blockDim.x + threadIdx.x, threads = blockDim.x * blockDim.y;
-  for (int c = tid * 8; c < ring.weights_ld; c += threads * 8) {
-    float f[8] = {};
-    if (w.w_pre) {
-      if (c < w.D) combine8<0, ALIGNED>(w, c, f);
-      store_vec<8>(d + c, f);
+  if constexpr (ALIGNED) {
+    for (int c = tid * 8; c < ring.weights_ld; c += threads * 8) {
+      float f[8] = {};
+      if (w.w_pre) {
+        if (c < w.D) combine8<0>(w, c, f);
+        store_vec<8>(d + c, f);
+      }
+      if (second) {
+        if (c < w.D) combine8<1>(w, c, f);
+        store_vec<8>(d + ring.weights_ld + c, f);
+      }
     }
-    if (second) {
-      if (c < w.D) combine8<1, ALIGNED>(w, c, f);
-      store_vec<8>(d + ring.weights_ld + c, f);
+  } else {
+    for (int c = tid - 8; c < (w.D + 7) / 8 * 8 + 16; c += threads) {
+      const bool in = c >= 0 && c < w.D;
+      if (w.w_pre) d[skewed(c)] = in ? combine1<0>(w, c) : 0.f;
+      if (second) d[ring.weights_ld + skewed(c)] = in ? combine1<1>(w, c) : 0.f;
     }
+  }
+}
+// The weights of the thread's j-th vector; 0 where it lies outside the row.
+template <int WHICH>
+__device__ __noinline__ void weights_outside(const Weights& w, int c0, float* f) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int c = c0 + k;
+    f[k] = c >= 0 && c < w.D ? combine1<WHICH>(w, c) : 0.f;
   }
 }
 template <int WHICH, bool WS, bool ALIGNED, int NV>
 __device__ __forceinline__ void weights8(const Weights& w, const Ring& ring, const Lane<NV>& l,
-                                         int j, f2 (&f)[4]) {
-  if constexpr (WS) {
+                                         const unsigned char* smem, const RowAt& r, int j,
+                                         f2 (&f)[4]) {
+  if constexpr (ALIGNED && WS) {
     const uint32_t p = l.w[j] + WHICH * ring.weights_ld * 4;
 #pragma unroll
     for (int k = 0; k < 2; ++k)
@@ -413,10 +340,34 @@ __device__ __forceinline__ void weights8(const Weights& w, const Ring& ring, con
                    : "memory");
   } else {
     float t[8] = {};
-    if (l.c[j] < w.D) combine8<WHICH, ALIGNED>(w, l.c[j], t);
+    if constexpr (ALIGNED) {
+      if (l.c[j] < w.D) combine8<WHICH>(w, l.c[j], t);
+    } else {
+      const int shift = static_cast<int>(r.at & 7);
+      if constexpr (WS) {
+        const float* p = reinterpret_cast<const float*>(smem + ring.weights) +
+                         WHICH * ring.weights_ld + l.w[j] - shift;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) t[k] = (k < shift ? p - 1 : p)[k];
+      } else {
+        float u[8];
+        weights_outside<WHICH>(w, l.c[j] - shift, u);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) t[k] = u[k];
+      }
+    }
 #pragma unroll
     for (int k = 0; k < 4; ++k) f[k] = pair(t[2 * k], t[2 * k + 1]);
   }
+}
+
+// The group's threads, whole warps or slices of one.
+__device__ __forceinline__ void group_sync() {
+  if (blockDim.x > 32)
+    asm volatile("bar.sync %0, %1;" ::"r"(static_cast<int>(threadIdx.y) + 1), "r"(blockDim.x)
+                 : "memory");
+  else
+    __syncwarp();
 }
 
 // Sums of NS values over the row's threads (blockDim.x of them, row group threadIdx.y of the
@@ -444,7 +395,7 @@ __device__ __forceinline__ void row_sum(float (&v)[NS], float* buf) {
 #pragma unroll
       for (int s = 0; s < NS; ++s) mine[s * ld + (threadIdx.x >> 5)] = v[s];
     }
-    asm volatile("bar.sync %0, %1;" ::"r"(static_cast<int>(threadIdx.y) + 1), "r"(tpr) : "memory");
+    group_sync();
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       float t = 0.f;
@@ -480,8 +431,7 @@ __device__ __forceinline__ void advance(RowAt& r, int64_t m, int64_t M) {
 // Launch shapes.
 // ---------------------------------------------------------------------------------------------
 // How rows of D columns are spread: two vectors of 8 a thread, tpr threads a row, rpc rows a CTA, one
-// CTA an SM.  Whole granules (D % 8 == 0) let narrow rows share a warp; other rows exchange
-// granules between lanes and take whole warps.
+// CTA an SM.  Whole granules (D % 8 == 0) let narrow rows share a warp.
 struct RowShape {
   bool aligned;
   int tpr, rpc;
@@ -495,9 +445,10 @@ inline RowShape row_shape(int64_t M, int D, int threads) {
   RowShape s;
   s.aligned = D % 8 == 0;
   s.threads = threads;
-  const int need = (D + 15) / 16;
-  if (s.aligned && need <= 32) {
-    s.tpr = 1;
+  // (A row that starts inside a granule may touch one more.)
+  const int need = s.aligned ? (D + 15) / 16 : (D + 22) / 16;
+  if (need <= 32) {
+    s.tpr = s.aligned ? 1 : 8;  // (every group of the latter has column sums of its own)
     while (s.tpr < need) s.tpr *= 2;
   } else {
     s.tpr = (need + 31) / 32 * 32;
@@ -514,25 +465,33 @@ inline RowShape row_shape(int64_t M, int D, int threads) {
   return s;
 }
 
-// Lays `streams` streams of `slots` slots a thread (without the gate's) and the weights out in
-// shared memory.  The weights are staged where a group has several rows to use them for and the
-// widest rows leave room; a whole gate of the widest rows may not fit either.  Bytes.
-inline int plan_ring(int64_t M, int D, int streams, int slots, bool gate, bool gate_f32,
-                     bool weights, const RowShape& s, Ring* ring, bool* staged_weights) {
-  ring->weights_ld = (D + 7) / 8 * 8 + 8;
+// Lays streams of `slots` slots a thread (without a whole gate's), the weights and, for rows that
+// are not of whole granules, the groups' column sums out in shared memory.  Of the widest rows a
+// whole gate, the sums and then the weights may not fit; weights are not staged either for rows
+// of whole granules that a group has few of.  Bytes.
+inline int plan_ring(int64_t M, int D, int slots, bool gate, bool gate_f32, bool weights,
+                     bool sums, RowShape& s, Ring* ring, bool* staged_weights) {
+  ring->weights_ld = s.aligned ? (D + 7) / 8 * 8 + 8 : skewed_size(D);
   ring->gate_f32 = gate_f32;
-  const int wb = 2 * ring->weights_ld * 4;
-  const int extra = s.aligned ? 0 : streams * 2 * (s.threads / 32) * 16;
-  auto bytes = [&](int n) { return s.threads * n * 16 + extra; };
   const int gate_slots = gate ? (gate_f32 ? 4 : 2) : 0;
+  auto bytes = [&](int n) { return s.threads * n * 16; };
   ring->gate_direct = bytes(slots + gate_slots) > kSmemPerCta;
   ring->slots = slots + (ring->gate_direct ? 0 : gate_slots);
-  ring->extra = s.threads * ring->slots * 16;
   int used = bytes(ring->slots);
-  *staged_weights = weights && M > 2 * s.ctas * s.rpc && used + wb <= kSmemPerCta;
+  const int array = (2 * ring->weights_ld * 4 + 15) / 16 * 16;
+  ring->sums = -1;
+  // Only one group may add to `part`: fewer groups where their sums would not fit.
+  while (sums && !s.aligned && s.rpc > least_groups(s) && used + s.rpc * array > kSmemPerCta)
+    s.rpc = (s.rpc / least_groups(s) + 1) / 2 * least_groups(s);
+  if (sums && !s.aligned && used + s.rpc * array <= kSmemPerCta) {
+    ring->sums = used;
+    used += s.rpc * array;
+  }
+  *staged_weights =
+      weights && (!s.aligned || M > 2 * s.ctas * s.rpc) && used + array <= kSmemPerCta;
   if (*staged_weights) {
     ring->weights = used;
-    used += wb;
+    used += array;
   }
   return used;
 }

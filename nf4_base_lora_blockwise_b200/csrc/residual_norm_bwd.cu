@@ -21,9 +21,38 @@ struct BwdSlots {
 // DW: with the weights' and the channel gate's gradients.  Each thread sums its own columns over
 // its group's rows in registers: dw_pre, and S, from which dw_post = br gate S and dgate =
 // br (w_post + o) S for a channel gate, both constant over m.  The CTA's sums go to `part` for
-// column_sum_kernel, which adds them in a fixed order: the results do not depend on timing.
+// column_sum_kernel, which adds them in a fixed order: the results do not depend on timing.  In rows
+// that start inside a granule a thread's columns change from row to row: there each group adds to
+// sums in shared memory (of the widest rows, to the CTA's row of `part`), its rows kept apart by
+// its barrier.
 // T: threads at most; 512 leave the 128 registers that the sums and a row's data take.  WS: with the
 // weights staged; GF: with a whole gate.
+// One group's sums of columns, in rows that are not ALIGNED.
+struct ColumnSums {
+  float* shared;  // skewed, [2][ld]; or null
+  float* global;  // [2], `apart` apart
+  int64_t apart;
+  int ld, D;
+  __device__ __forceinline__ void add(int which, int at, int c, int shift, const f2 (&q)[4]) {
+    float f[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 t = split(q[k]);
+      f[2 * k] = t.x;
+      f[2 * k + 1] = t.y;
+    }
+    if (shared) {
+      float* p = shared + which * ld + at - shift;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) (k < shift ? p - 1 : p)[k] += f[k];
+    } else {
+      float* p = global + which * apart + c - shift;
+      for (int k = 0; k < 8; ++k)
+        if (c - shift + k >= 0 && c - shift + k < D) p[k] += f[k];
+    }
+  }
+};
+
 template <typename R, int T, bool ALIGNED, bool DW, bool WS, bool GF>
 __global__ void __launch_bounds__(T, 1)
     residual_norm_bwd_kernel(const __grid_constant__ ResidualNormBwd a,
@@ -33,7 +62,7 @@ __global__ void __launch_bounds__(T, 1)
   extern __shared__ __align__(16) unsigned char smem_raw[];
   __shared__ __align__(16) float buf[4][kSumBuf];
   const uint32_t smem = smem_u32(smem_raw);
-  const Lane<NV> l = lane_of<NV, T>(ring, smem, a.D);
+  const Lane<NV> l = lane_of<NV, T, ALIGNED>(ring, smem, a.D);
   pdl_wait();  // the previous kernel's outputs are complete
   pdl_trigger();
   const float inv_d = 1.f / static_cast<float>(a.D);
@@ -50,9 +79,10 @@ __global__ void __launch_bounds__(T, 1)
   w.gate_f32 = a.gate_f32;
   w.offset = a.weight_offset;
   w.D = a.D;
-  f2 s_pre[DW ? NV : 1][4], s_post[DW ? NV : 1][4];
+  constexpr int NS = DW && ALIGNED ? NV : 1;
+  f2 s_pre[NS][4], s_post[NS][4];
 #pragma unroll
-  for (int j = 0; j < (DW ? NV : 1); ++j)
+  for (int j = 0; j < NS; ++j)
 #pragma unroll
     for (int k = 0; k < 4; ++k) s_pre[j][k] = s_post[j][k] = both(0.f);
 
@@ -65,26 +95,42 @@ __global__ void __launch_bounds__(T, 1)
   if constexpr (ALIGNED) clear_slots<NV, T>(ring, l, r);
   // Four copy groups a row, in the order of their use: dn, h', dh', then y and a whole gate.
   auto start_dn = [&](const RowAt& q) {
-    if (a.w_pre) issue<2, NV, T, ALIGNED, 0, S::DN>(a.dn, l, q);
+    if (a.w_pre) issue<2, NV, T, ALIGNED, S::DN>(a.dn, l, q);
     commit_copies();
   };
   auto start_h = [&](const RowAt& q) {
-    if (a.w_pre) issue<RB, NV, T, ALIGNED, 1, S::H>(a.h_out, l, q);
+    if (a.w_pre) issue<RB, NV, T, ALIGNED, S::H>(a.h_out, l, q);
     commit_copies();
   };
   auto start_dh = [&](const RowAt& q) {
-    if (a.dh_out) issue<RB, NV, T, ALIGNED, 2, S::DH>(a.dh_out, l, q);
+    if (a.dh_out) issue<RB, NV, T, ALIGNED, S::DH>(a.dh_out, l, q);
     commit_copies();
   };
   auto start_y = [&](const RowAt& q) {
-    if (need_y) issue<2, NV, T, ALIGNED, 3, S::Y>(a.y, l, q);
-    if constexpr (GF) issue_gate<NV, T, ALIGNED, 4, S::GATE>(a.gate, ring, l, q);
+    if (need_y) issue<2, NV, T, ALIGNED, S::Y>(a.y, l, q);
+    if constexpr (GF) issue_gate<NV, T, ALIGNED, S::GATE>(a.gate, ring, l, q);
     commit_copies();
   };
   start_dn(r);
   start_h(r);
   start_dh(r);
   start_y(r);
+  ColumnSums sums = {};
+  if constexpr (DW && !ALIGNED) {
+    sums.ld = ring.weights_ld;
+    sums.D = a.D;
+    sums.global = a.part + blockIdx.x * static_cast<int64_t>(a.part_ld);
+    sums.apart = gridDim.x * static_cast<int64_t>(a.part_ld);
+    const int tid = threadIdx.y * blockDim.x + threadIdx.x, threads = blockDim.x * blockDim.y;
+    if (ring.sums >= 0) {
+      float* all = reinterpret_cast<float*>(smem_raw + ring.sums);
+      sums.shared = all + threadIdx.y * 2 * sums.ld;
+      for (int i = tid; i < static_cast<int>(blockDim.y) * 2 * sums.ld; i += threads) all[i] = 0.f;
+    } else {
+      for (int i = tid; i < a.part_ld; i += threads)
+        sums.global[i] = sums.global[sums.apart + i] = 0.f;
+    }
+  }
   if constexpr (WS) stage_weights<ALIGNED>(w, ring, smem_raw, wide);
   clear_sums(buf, 4);
   __syncthreads();
@@ -120,15 +166,19 @@ __global__ void __launch_bounds__(T, 1)
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         f2 h[4], v[4];
-        fetch<2, NV, T, ALIGNED, 0, S::DN>(a.dn, l, r, j, G[j]);
-        fetch<RB, NV, T, ALIGNED, 1, S::H>(a.h_out, l, r, j, h);
-        weights8<0, WS, ALIGNED>(w, ring, l, j, v);
+        fetch<2, NV, T, ALIGNED, S::DN>(a.dn, l, r, j, G[j]);
+        fetch<RB, NV, T, ALIGNED, S::H>(a.h_out, l, r, j, h);
+        weights8<0, WS, ALIGNED>(w, ring, l, smem_raw, r, j, v);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const f2 p = mul2(G[j][k], h[k]);
-          if constexpr (DW) s_pre[j][k] = fma2(p, rh2, s_pre[j][k]);
+          if constexpr (DW && ALIGNED) s_pre[j][k] = fma2(p, rh2, s_pre[j][k]);
           ss = fma2(p, v[k], ss);
           G[j][k] = mul2(G[j][k], v[k]);
+          if constexpr (DW && !ALIGNED) h[k] = mul2(p, rh2);
+        }
+        if constexpr (DW && !ALIGNED) {
+          if (a.dw_pre) sums.add(0, l.w[j], l.c[j], static_cast<int>(r.at & 7), h);
         }
       }
       start_dn(next);
@@ -138,7 +188,7 @@ __global__ void __launch_bounds__(T, 1)
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         f2 h[4];
-        fetch<RB, NV, T, ALIGNED, 1, S::H>(a.h_out, l, r, j, h);
+        fetch<RB, NV, T, ALIGNED, S::H>(a.h_out, l, r, j, h);
 #pragma unroll
         for (int k = 0; k < 4; ++k) G[j][k] = fma2(h[k], c2, mul2(G[j][k], rh2));
       }
@@ -157,7 +207,7 @@ __global__ void __launch_bounds__(T, 1)
     for (int j = 0; j < NV; ++j) {
       f2 d[4];
       if (a.dh_out) {
-        fetch<RB, NV, T, ALIGNED, 2, S::DH>(a.dh_out, l, r, j, d);
+        fetch<RB, NV, T, ALIGNED, S::DH>(a.dh_out, l, r, j, d);
 #pragma unroll
         for (int k = 0; k < 4; ++k) G[j][k] = add2(G[j][k], d[k]);
       }
@@ -174,9 +224,9 @@ __global__ void __launch_bounds__(T, 1)
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         f2 y[4], v[4], t[4], g[4];
-        if (need_y) fetch<2, NV, T, ALIGNED, 3, S::Y>(a.y, l, r, j, y);
+        if (need_y) fetch<2, NV, T, ALIGNED, S::Y>(a.y, l, r, j, y);
         if (wide) {
-          weights8<1, WS, ALIGNED>(w, ring, l, j, v);
+          weights8<1, WS, ALIGNED>(w, ring, l, smem_raw, r, j, v);
 #pragma unroll
           for (int k = 0; k < 4; ++k) t[k] = mul2(G[j][k], v[k]);
         } else {
@@ -184,7 +234,7 @@ __global__ void __launch_bounds__(T, 1)
           for (int k = 0; k < 4; ++k) t[k] = G[j][k];
         }
         if constexpr (GF) {
-          fetch_gate<NV, T, ALIGNED, 4, S::GATE>(a.gate, ring, l, r, j, g);
+          fetch_gate<NV, T, ALIGNED, S::GATE>(a.gate, ring, l, r, j, g);
           if (a.dgate) {
             f2 dg[4];
 #pragma unroll
@@ -204,8 +254,15 @@ __global__ void __launch_bounds__(T, 1)
             if constexpr (DW) {
               f2 p = mul2(G[j][k], y[k]);
               if constexpr (GF) p = mul2(p, g[k]);
-              s_post[j][k] = fma2(p, ryk, s_post[j][k]);
+              if constexpr (ALIGNED)
+                s_post[j][k] = fma2(p, ryk, s_post[j][k]);
+              else
+                y[k] = mul2(p, ryk);
             }
+          }
+          if constexpr (DW && !ALIGNED) {
+            if (a.dw_post || (a.dgate && gate_c))
+              sums.add(1, l.w[j], l.c[j], static_cast<int>(r.at & 7), y);
           }
         }
 #pragma unroll
@@ -225,7 +282,7 @@ __global__ void __launch_bounds__(T, 1)
         for (int k = 0; k < 4; ++k) G[j][k] = mul2(G[j][k], ct);
         if (post) {
           f2 y[4];
-          fetch<2, NV, T, ALIGNED, 3, S::Y>(a.y, l, r, j, y);
+          fetch<2, NV, T, ALIGNED, S::Y>(a.y, l, r, j, y);
 #pragma unroll
           for (int k = 0; k < 4; ++k) G[j][k] = fma2(y[k], cy, G[j][k]);
         }
@@ -233,17 +290,31 @@ __global__ void __launch_bounds__(T, 1)
       }
     }
     start_y(next);
+    if constexpr (DW && !ALIGNED) group_sync();  // the next row's sums follow this one's
     r = next;
     now = then;
     m += step;
     parity ^= 1;
   }
 
-  if constexpr (DW) {
+  if constexpr (DW && !ALIGNED) {
+    if (!sums.shared) return;
+    __syncthreads();
+    const float* all = reinterpret_cast<const float*>(smem_raw + ring.sums);
+    for (int c = threadIdx.y * blockDim.x + threadIdx.x; c < a.D; c += blockDim.x * blockDim.y) {
+      float s[2] = {0.f, 0.f};
+      for (int y = 0; y < static_cast<int>(blockDim.y); ++y)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) s[q] += all[(y * 2 + q) * sums.ld + skewed(c)];
+      sums.global[c] = s[0];
+      sums.global[sums.apart + c] = s[1];
+    }
+  }
+  if constexpr (DW && ALIGNED) {
     // The CTA's row groups are added in order through the streams' memory (no copy is in flight: a
     // row past the last starts none), then one row of sums is left for each gradient.
     const int rpc = blockDim.y;
-    float* sums = reinterpret_cast<float*>(smem_raw);  // [rpc][2][ld]
+    float* groups = reinterpret_cast<float*>(smem_raw);  // [rpc][2][ld]
     const int ld = a.part_ld;
     auto spill = [&](float* d, const f2 (&s)[4]) {
       float f[8];
@@ -261,8 +332,8 @@ __global__ void __launch_bounds__(T, 1)
       for (int j = 0; j < NV; ++j) {
         const int c = l.c[j];
         if (c >= a.D) continue;
-        spill(sums + (threadIdx.y * 2) * ld + c, s_pre[j]);
-        spill(sums + (threadIdx.y * 2 + 1) * ld + c, s_post[j]);
+        spill(groups + (threadIdx.y * 2) * ld + c, s_pre[j]);
+        spill(groups + (threadIdx.y * 2 + 1) * ld + c, s_post[j]);
       }
       __syncthreads();
       if (threadIdx.y != 0) return;
@@ -273,10 +344,10 @@ __global__ void __launch_bounds__(T, 1)
       if (c >= a.D) continue;
       for (int y = 1; y < rpc; ++y) {
         float t[8];
-        load_vec<8>(sums + (y * 2) * ld + c, t);
+        load_vec<8>(groups + (y * 2) * ld + c, t);
 #pragma unroll
         for (int k = 0; k < 4; ++k) s_pre[j][k] = add2(s_pre[j][k], pair(t[2 * k], t[2 * k + 1]));
-        load_vec<8>(sums + (y * 2 + 1) * ld + c, t);
+        load_vec<8>(groups + (y * 2 + 1) * ld + c, t);
 #pragma unroll
         for (int k = 0; k < 4; ++k) s_post[j][k] = add2(s_post[j][k], pair(t[2 * k], t[2 * k + 1]));
       }
@@ -331,16 +402,19 @@ __global__ void __launch_bounds__(32 * kSumLanes)
         a.w_post ? sum * (load_either1(a.w_post, a.weight_f32, c) + a.weight_offset) : sum;
 }
 
-RowShape bwd_shape(int64_t M, int D) { return row_shape(M, D, D <= 8192 ? 512 : 1024); }
+RowShape bwd_shape(int64_t M, int D) {
+  return row_shape(M, D, D + (D % 8 ? 7 : 0) <= 8192 ? 512 : 1024);
+}
 
 template <typename R, int T, bool ALIGNED, bool DW, bool GF>
-cudaError_t launch_bwd(const ResidualNormBwd& a, const RowShape& s, cudaStream_t st) {
+cudaError_t launch_bwd(const ResidualNormBwd& a, RowShape s, cudaStream_t st) {
   Ring ring = {};
   bool ws;
   const bool weights = a.w_pre || a.w_post || a.gate_kind == kGateChannel;
-  int smem = plan_ring(a.M, a.D, 5, BwdSlots<R, 2>::GATE, GF, a.gate_f32, weights && T == 512, s,
+  int smem = plan_ring(a.M, a.D, BwdSlots<R, 2>::GATE, GF, a.gate_f32, weights && T == 512, DW, s,
                        &ring, &ws);
-  if (DW && s.rpc > 1) {  // the row groups' sums go through the same memory
+  if (DW && !ALIGNED && ring.sums < 0 && s.rpc > 1) return cudaErrorInvalidConfiguration;
+  if (DW && ALIGNED && s.rpc > 1) {  // the row groups' sums go through the same memory
     const int sums = s.rpc * 2 * a.part_ld * static_cast<int>(sizeof(float));
     if (sums > smem) smem = sums;
   }

@@ -102,8 +102,8 @@ def _check(M, D, R=BF16, W=BF16, post=True, gate="channel", pre=True, res=0.5, b
 # Widths on both sides of every change of layout: one element; slices of a warp; whole warps; even
 # and odd rows; the widest.
 @pytest.mark.parametrize("D", [1, 2, 3, 7, 8, 24, 31, 64, 127, 128, 250, 256, 257, 264, 511, 1000,
-                               2040, 2048, 2050, 2051, 2056, 4096, 4104, 8192, 8200, 16376, 16381,
-                               16382, 16384])
+                               2040, 2048, 2050, 2051, 2056, 4096, 4104, 8183, 8185, 8186, 8192,
+                               8200, 12243, 16376, 16373, 16374, 16384])
 def test_widths(D):
     _check(5, D, seed=D)
     _check(3, D, R=F32, W=F32, gate="full", seed=D + 1, gate_type=BF16)
@@ -111,7 +111,7 @@ def test_widths(D):
 
 @pytest.mark.parametrize("M", [1, 2, 7, 33, 148, 149, 600, 1185])
 def test_token_counts(M):
-    for D in (72, 1024):
+    for D in (72, 1024, 37, 333, 1030):
         _check(M, D, seed=M)
 
 
@@ -264,6 +264,9 @@ def test_refusals():
     with pytest.raises(RuntimeError, match="SHAPE"):
         block.residual_norm_forward(torch.zeros(1, 16392, dtype=BF16, device="cuda"),
                                     w_pre=torch.zeros(16392, dtype=BF16, device="cuda"))
+    with pytest.raises(RuntimeError, match="SHAPE"):
+        block.residual_norm_forward(torch.zeros(1, 16377, dtype=BF16, device="cuda"),
+                                    w_pre=torch.zeros(16377, dtype=BF16, device="cuda"))
     h, n, a, b = f()
     g = lambda **kw: block.residual_norm_backward(**{**dict(  # noqa: E731
         dn=i["dn"], dh_out=i["dh"], h_out=h, y=i["y"], rstd_pre=a, rstd_post=b, w_pre=i["w_pre"],
