@@ -372,8 +372,8 @@ cudaError_t launch_swiglu_packed_bwd(const __nv_bfloat16* gu, const __nv_bfloat1
 
 // ------------------------------ residual update with its norms ------------------------------
 enum GateKind { kGateNone = 0, kGateChannel = 1, kGateToken = 2, kGateFull = 3 };
-constexpr int kNormMaxD = 16384;  // 1024 threads of 16 elements; rows of D % 8 != 0 may start inside
-                                  // a granule of 8 and take one more: up to 16376
+constexpr int kNormMaxD = 16384;  // two CTAs of 512 threads of 16 elements; rows of D % 8 != 0 may
+                                  // start inside a granule of 8 and take one more: up to 16376
 struct ResidualNormFwd {
   const void* h;           // [M, D] fp32 when resid_f32, else bf16
   const __nv_bfloat16* y;  // [M, D] or null: h goes to the norm as it is

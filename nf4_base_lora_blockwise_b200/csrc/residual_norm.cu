@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   extern __shared__ __align__(16) unsigned char smem_raw[];
   __shared__ __align__(16) float buf[4][kSumBuf];
   const uint32_t smem = smem_u32(smem_raw);
-  const Lane<NV> l = lane_of<NV, T, ALIGNED>(ring, smem, a.D);
+  const Lane<NV> l = lane_of<NV, T, ALIGNED, false>(ring, smem, a.D);
   pdl_wait();  // the previous kernel's outputs are complete
   pdl_trigger();
   const float inv_d = 1.f / static_cast<float>(a.D);
@@ -58,11 +58,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   w.offset = a.weight_offset;
   w.D = a.D;
 
+  const int64_t walker = blockIdx.x;
   const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;
   RowAt r, next;
   r.total = next.total = a.M * a.D;
   r.D = next.D = a.D;
-  int64_t m = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  int64_t m = walker * blockDim.y + threadIdx.y;
   advance(r, m, a.M);
   if constexpr (ALIGNED) clear_slots<NV, T>(ring, l, r);
   // Two copy groups a row: y, then h and a whole gate.
@@ -77,7 +78,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   };
   start_y(r);
   start_h(r);
-  if constexpr (WS) stage_weights<ALIGNED>(w, ring, smem_raw, wide);
+  if constexpr (WS) stage_weights<ALIGNED, false>(w, ring, smem_raw, wide);
   clear_sums(buf, 4);
   __syncthreads();
 
@@ -89,7 +90,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 
   // The same number of rounds for every group, so that a warp's slices stay together.
   int parity = 0;
-  for (int64_t base = static_cast<int64_t>(blockIdx.x) * blockDim.y; base < a.M; base += step) {
+  for (int64_t base = walker * blockDim.y; base < a.M; base += step) {
     advance(next, m + step, a.M);
     const float then = token_of(next, m + step);
     f2 h[NV][4];
@@ -106,10 +107,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       start_y(next);
       float scale = a.branch_scale * token;
       if (a.w_post) {
-        float s[1] = {sum2(ss)};
-        row_sum<1>(s, buf[parity * 2]);
-        const float rs = rsqrtf(s[0] * inv_d + a.eps);
-        if (r.row && threadIdx.x == 0 && a.rstd_post) a.rstd_post[m] = rs;
+        const float rs = rsqrtf(row_sum<false>(sum2(ss), buf[parity * 2]) * inv_d + a.eps);
+        if (r.row && l.c[0] == 0 && a.rstd_post) a.rstd_post[m] = rs;
         scale *= rs;
       }
       wait_copies<1>();
@@ -149,10 +148,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int k = 0; k < 4; ++k) ss = fma2(h[j][k], h[j][k], ss);
-      float s[1] = {sum2(ss)};
-      row_sum<1>(s, buf[parity * 2 + 1]);
-      const float rs = rsqrtf(s[0] * inv_d + a.eps);
-      if (r.row && threadIdx.x == 0 && a.rstd_pre) a.rstd_pre[m] = rs;
+      const float rs = rsqrtf(row_sum<false>(sum2(ss), buf[parity * 2 + 1]) * inv_d + a.eps);
+      if (r.row && l.c[0] == 0 && a.rstd_pre) a.rstd_pre[m] = rs;
       const f2 rr = both(rs);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
@@ -170,25 +167,22 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   }
 }
 
-template <typename R, bool ALIGNED>
+template <typename R, bool ALIGNED, bool GF>
 cudaError_t launch_fwd(const ResidualNormFwd& a, RowShape s, cudaStream_t st) {
   Ring ring = {};
   bool ws;
   const bool weights = a.w_pre || a.w_post || a.gate_kind == kGateChannel;
-  const bool gf = a.gate_kind == kGateFull;
-  const int smem = plan_ring(a.M, a.D, FwdSlots<R, 2>::GATE, gf, a.gate_f32, weights, false, s,
+  const int smem = plan_ring(a.M, a.D, FwdSlots<R, 2>::GATE, GF, a.gate_f32, weights, false, s,
                              &ring, &ws);
-  if (gf)
-    return ws ? launch_rows(residual_norm_fwd_kernel<R, ALIGNED, true, true>, s, a, ring, smem, st)
-              : launch_rows(residual_norm_fwd_kernel<R, ALIGNED, false, true>, s, a, ring, smem,
-                            st);
-  return ws ? launch_rows(residual_norm_fwd_kernel<R, ALIGNED, true, false>, s, a, ring, smem, st)
-            : launch_rows(residual_norm_fwd_kernel<R, ALIGNED, false, false>, s, a, ring, smem, st);
+  return ws ? launch_rows(residual_norm_fwd_kernel<R, ALIGNED, true, GF>, s, a, ring, smem, st)
+            : launch_rows(residual_norm_fwd_kernel<R, ALIGNED, false, GF>, s, a, ring, smem, st);
 }
 template <typename R>
 cudaError_t launch_fwd(const ResidualNormFwd& a, cudaStream_t st) {
-  const RowShape s = row_shape(a.M, a.D, kFwdThreads);
-  return s.aligned ? launch_fwd<R, true>(a, s, st) : launch_fwd<R, false>(a, s, st);
+  const RowShape s = row_shape(a.M, a.D, kFwdThreads, false);
+  if (a.gate_kind == kGateFull)
+    return s.aligned ? launch_fwd<R, true, true>(a, s, st) : launch_fwd<R, false, true>(a, s, st);
+  return s.aligned ? launch_fwd<R, true, false>(a, s, st) : launch_fwd<R, false, false>(a, s, st);
 }
 
 }  // namespace

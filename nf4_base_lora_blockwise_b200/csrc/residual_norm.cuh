@@ -15,6 +15,34 @@ namespace qlora {
 namespace {
 
 // ---------------------------------------------------------------------------------------------
+// Groups and pairs.
+// ---------------------------------------------------------------------------------------------
+__device__ __forceinline__ void st_peer(float* p, uint32_t rank, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(mapa_shared(smem_u32(p), rank)), "f"(v) : "memory");
+}
+__device__ __forceinline__ float ld_peer(const float* p, uint32_t rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(smem_u32(p), rank)) : "memory");
+  return v;
+}
+template <bool PAIR>
+__device__ __forceinline__ void all_sync() {
+  if constexpr (PAIR)
+    cluster_sync_all();
+  else
+    __syncthreads();
+}
+
+// The group's threads, whole warps or slices of one.
+__device__ __forceinline__ void group_sync() {
+  if (blockDim.x > 32)
+    asm volatile("bar.sync %0, %1;" ::"r"(static_cast<int>(threadIdx.y) + 1), "r"(blockDim.x)
+                 : "memory");
+  else
+    __syncwarp();
+}
+
+// ---------------------------------------------------------------------------------------------
 // Row streams: [M, D] tensors read row by row.  Every thread has `slots` 16-byte slots in shared
 // memory, [slot][T threads] (a copy whose lanes do not write one contiguous piece of shared memory
 // measured a third slower); a stream's, and the T that a CTA has room for, are given at compile
@@ -25,11 +53,18 @@ namespace {
 // first one: columns 8 v - shift .. 8 v - shift + 7, where there are such columns.  All streams
 // and outputs share that, so whole granules are read and stored as they lie, but for a row's
 // ends; only what belongs to columns (weights, column sums) is addressed by column.
+//
+// PAIR (backward): rows wider than 8192 columns are shared by a cluster of two CTAs, half the
+// vectors each, where 1024 threads of one CTA would leave too few registers or too little shared
+// memory for column sums or weights; a row's sums cross through each other's shared memory with
+// a barrier of the cluster.  (1024 x 16384 with column sums 91 -> 70 us; without them, and
+// forward, one CTA a row measured 45 and 31 us against a pair's 62 and 47.)
 // ---------------------------------------------------------------------------------------------
 struct Ring {
   int slots;       // of a thread
   int weights;     // byte of the combined weights' [2][weights_ld] fp32
-  int weights_ld;  // D rounded up to 8, and 8 zeros; or skewed_size(D)
+  int width;       // of the CTA's part of a row: D rounded up to 8, or 16 columns a thread
+  int weights_ld;  // width and 8 zeros; or skewed_size(width)
   int sums;        // byte of the column sums' [group][2][weights_ld] fp32, or -1: in `part`
   int gate_f32;    // a whole gate's type
   int gate_direct; // a whole gate that does not fit: read from global memory where it is used
@@ -90,21 +125,27 @@ struct Lane {
   uint32_t w[NV];  // ALIGNED: of the combined weights of its columns; else vector v's skewed index
   int c[NV];       // 8 v
 };
-template <int NV, int T, bool ALIGNED>
+// First column (or 8 v) of the CTA's part of a row.
+template <bool PAIR>
+__device__ __forceinline__ int part_first(const Ring& ring) {
+  return PAIR ? static_cast<int>(cluster_ctarank()) * ring.width : 0;
+}
+template <int NV, int T, bool ALIGNED, bool PAIR>
 __device__ __forceinline__ Lane<NV> lane_of(const Ring& ring, uint32_t smem, int D) {
   const int tid = threadIdx.y * blockDim.x + threadIdx.x;
   Lane<NV> l;
   l.slots = smem + tid * 16;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
-    l.c[j] = (j * blockDim.x + threadIdx.x) * 8;
+    const int here = (j * blockDim.x + threadIdx.x) * 8;
+    l.c[j] = part_first<PAIR>(ring) + here;
     if constexpr (ALIGNED) {
       // Past the row's end: the zeros behind the weights.
-      const int at = l.c[j] < D ? l.c[j] : ring.weights_ld - 8;
+      const int at = l.c[j] < D ? here : ring.width;
       l.w[j] = smem + ring.weights + at * 4;
     } else {
-      const int last = (D + 7) / 8 * 8 + 8;  // its columns are past the end for every shift
-      l.w[j] = (l.c[j] < last ? l.c[j] : last) / 8 * 9 + 9;
+      const int last = ring.width + 8;  // its columns are past the end for every shift
+      l.w[j] = (here < last ? here : last) / 8 * 9 + 9;
     }
   }
   return l;
@@ -292,28 +333,30 @@ __device__ __forceinline__ void combine8(const Weights& w, int c, float (&f)[8])
   }
 }
 // Fills the CTA's shared copy (a barrier follows before the first use).
-template <bool ALIGNED>
+template <bool ALIGNED, bool PAIR>
 __device__ __forceinline__ void stage_weights(const Weights& w, const Ring& ring,
                                               unsigned char* smem, bool second) {
+  const int first = part_first<PAIR>(ring);
   float* d = reinterpret_cast<float*>(smem + ring.weights);
   const int tid = threadIdx.y * blockDim.x + threadIdx.x, threads = blockDim.x * blockDim.y;
   if constexpr (ALIGNED) {
     for (int c = tid * 8; c < ring.weights_ld; c += threads * 8) {
       float f[8] = {};
+      const bool in = c < ring.width && first + c < w.D;
       if (w.w_pre) {
-        if (c < w.D) combine8<0>(w, c, f);
+        if (in) combine8<0>(w, first + c, f);
         store_vec<8>(d + c, f);
       }
       if (second) {
-        if (c < w.D) combine8<1>(w, c, f);
+        if (in) combine8<1>(w, first + c, f);
         store_vec<8>(d + ring.weights_ld + c, f);
       }
     }
   } else {
-    for (int c = tid - 8; c < (w.D + 7) / 8 * 8 + 16; c += threads) {
-      const bool in = c >= 0 && c < w.D;
-      if (w.w_pre) d[skewed(c)] = in ? combine1<0>(w, c) : 0.f;
-      if (second) d[ring.weights_ld + skewed(c)] = in ? combine1<1>(w, c) : 0.f;
+    for (int c = tid - 8; c < ring.width + 16; c += threads) {
+      const bool in = first + c >= 0 && first + c < w.D;
+      if (w.w_pre) d[skewed(c)] = in ? combine1<0>(w, first + c) : 0.f;
+      if (second) d[ring.weights_ld + skewed(c)] = in ? combine1<1>(w, first + c) : 0.f;
     }
   }
 }
@@ -361,53 +404,39 @@ __device__ __forceinline__ void weights8(const Weights& w, const Ring& ring, con
   }
 }
 
-// The group's threads, whole warps or slices of one.
-__device__ __forceinline__ void group_sync() {
-  if (blockDim.x > 32)
-    asm volatile("bar.sync %0, %1;" ::"r"(static_cast<int>(threadIdx.y) + 1), "r"(blockDim.x)
-                 : "memory");
-  else
-    __syncwarp();
-}
-
-// Sums of NS values over the row's threads (blockDim.x of them, row group threadIdx.y of the
-// CTA); the result in every thread.  Past one warp the warps' sums go through `buf`, which the
-// group's next call with the same buf may overwrite only after another barrier: callers
-// alternate.  Each group has its own barrier (1 + its number; past one warp there are at most 8).
-template <int NS>
-__device__ __forceinline__ void row_sum(float (&v)[NS], float* buf) {
+// The sum of v over the row's threads (row group threadIdx.y of the CTA, or of both CTAs of a PAIR);
+// the result in every thread.  Past one warp the warps' sums go through `buf`, which the group's
+// next call with the same buf may overwrite only after another barrier: callers alternate.
+template <bool PAIR>
+__device__ __forceinline__ float row_sum(float v, float* buf) {
   const int tpr = blockDim.x;
   if (tpr >= 32) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-      for (int s = 0; s < NS; ++s) v[s] += __shfl_xor_sync(0xFFFFFFFFu, v[s], o);
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   } else {
-    for (int o = tpr / 2; o > 0; o >>= 1)
-#pragma unroll
-      for (int s = 0; s < NS; ++s) v[s] += __shfl_xor_sync(0xFFFFFFFFu, v[s], o);
+    for (int o = tpr / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   }
-  if (tpr > 32) {
-    // [group][NS][warps rounded up to 4], the padding zero from the kernel's start.
-    const int warps = tpr >> 5, ld = (warps + 3) & ~3;
-    float* mine = buf + threadIdx.y * NS * ld;
-    if ((threadIdx.x & 31) == 0) {
-#pragma unroll
-      for (int s = 0; s < NS; ++s) mine[s * ld + (threadIdx.x >> 5)] = v[s];
-    }
+  if (!PAIR && tpr <= 32) return v;
+  // [group][CTA of the pair][warps rounded up to 4], the padding zero from the kernel's start.
+  const int warps = tpr >> 5, ld = (warps + 3) & ~3, all = PAIR ? 2 * ld : ld;
+  float* mine = buf + threadIdx.y * all;
+  if ((threadIdx.x & 31) == 0) {
+    float* at = mine + (PAIR ? cluster_ctarank() * ld : 0) + (threadIdx.x >> 5);
+    *at = v;
+    if constexpr (PAIR) st_peer(at, cluster_ctarank() ^ 1u, v);
+  }
+  if constexpr (PAIR)
+    cluster_sync_all();
+  else
     group_sync();
-#pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      float t = 0.f;
-      for (int i = 0; i < ld; i += 4) {
-        const float4 q = *reinterpret_cast<const float4*>(mine + s * ld + i);
-        t += (q.x + q.y) + (q.z + q.w);
-      }
-      v[s] = t;
-    }
+  v = 0.f;
+  for (int i = 0; i < all; i += 4) {
+    const float4 q = *reinterpret_cast<const float4*>(mine + i);
+    v += (q.x + q.y) + (q.z + q.w);
   }
+  return v;
 }
-constexpr int kSumBuf = 2 * 48;  // floats of one buffer: 2 values, 32 warps padded to 4 a group
+constexpr int kSumBuf = 96;  // floats of one buffer
 __device__ __forceinline__ void clear_sums(float (*buf)[kSumBuf], int n) {
   const int tid = threadIdx.y * blockDim.x + threadIdx.x;
   for (int i = tid; i < n * kSumBuf; i += blockDim.x * blockDim.y) (&buf[0][0])[i] = 0.f;
@@ -433,20 +462,22 @@ __device__ __forceinline__ void advance(RowAt& r, int64_t m, int64_t M) {
 // How rows of D columns are spread: two vectors of 8 a thread, tpr threads a row, rpc rows a CTA, one
 // CTA an SM.  Whole granules (D % 8 == 0) let narrow rows share a warp.
 struct RowShape {
-  bool aligned;
-  int tpr, rpc;
-  int threads;  // that a CTA has room for
-  int64_t ctas;
+  bool aligned, pair;
+  int tpr, rpc;     // tpr: of one CTA
+  int threads;      // that a CTA has room for
+  int64_t walkers;  // CTAs, or pairs, that walk the rows
 };
 constexpr int kSms = 148;
 constexpr int kSmemPerCta = 222 * 1024;
 inline int least_groups(const RowShape& s) { return s.tpr >= 32 ? 1 : 32 / s.tpr; }  // whole warps
-inline RowShape row_shape(int64_t M, int D, int threads) {
+inline RowShape row_shape(int64_t M, int D, int threads, bool pair) {
   RowShape s;
   s.aligned = D % 8 == 0;
   s.threads = threads;
   // (A row that starts inside a granule may touch one more.)
-  const int need = s.aligned ? (D + 15) / 16 : (D + 22) / 16;
+  const int vectors = s.aligned ? D / 8 : (D + 14) / 8;
+  s.pair = pair;
+  const int need = (vectors + (s.pair ? 3 : 1)) / (s.pair ? 4 : 2);
   if (need <= 32) {
     s.tpr = s.aligned ? 1 : 8;  // (every group of the latter has column sums of its own)
     while (s.tpr < need) s.tpr *= 2;
@@ -457,11 +488,12 @@ inline RowShape row_shape(int64_t M, int D, int threads) {
   // barriers), no more than spreads the rows over every SM.
   s.rpc = threads / s.tpr;
   if (s.tpr > 32 && s.rpc > 8) s.rpc = 8;
-  const int64_t spread = (M + kSms - 1) / kSms;
+  const int sms = s.pair ? kSms / 2 : kSms;
+  const int64_t spread = (M + sms - 1) / sms;
   const int least = least_groups(s);
   if (s.rpc > spread) s.rpc = static_cast<int>((spread + least - 1) / least * least);
   const int64_t want = (M + s.rpc - 1) / s.rpc;
-  s.ctas = want < kSms ? want : kSms;
+  s.walkers = want < sms ? want : sms;
   return s;
 }
 
@@ -471,7 +503,8 @@ inline RowShape row_shape(int64_t M, int D, int threads) {
 // of whole granules that a group has few of.  Bytes.
 inline int plan_ring(int64_t M, int D, int slots, bool gate, bool gate_f32, bool weights,
                      bool sums, RowShape& s, Ring* ring, bool* staged_weights) {
-  ring->weights_ld = s.aligned ? (D + 7) / 8 * 8 + 8 : skewed_size(D);
+  ring->width = s.pair ? 16 * s.tpr : (D + 7) / 8 * 8;
+  ring->weights_ld = s.aligned ? ring->width + 8 : skewed_size(ring->width);
   ring->gate_f32 = gate_f32;
   const int gate_slots = gate ? (gate_f32 ? 4 : 2) : 0;
   auto bytes = [&](int n) { return s.threads * n * 16; };
@@ -488,7 +521,7 @@ inline int plan_ring(int64_t M, int D, int slots, bool gate, bool gate_f32, bool
     used += s.rpc * array;
   }
   *staged_weights =
-      weights && (!s.aligned || M > 2 * s.ctas * s.rpc) && used + array <= kSmemPerCta;
+      weights && (!s.aligned || M > 2 * s.walkers * s.rpc) && used + array <= kSmemPerCta;
   if (*staged_weights) {
     ring->weights = used;
     used += array;
@@ -504,8 +537,9 @@ cudaError_t launch_rows(K kernel, const RowShape& s, const A& a, const Ring& rin
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  return launch_pdl(kernel, dim3(static_cast<unsigned>(s.ctas)), dim3(s.tpr, s.rpc),
-                    static_cast<size_t>(smem), stream, 1, a, ring);
+  const int cluster = s.pair ? 2 : 1;
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(s.walkers * cluster)), dim3(s.tpr, s.rpc),
+                    static_cast<size_t>(smem), stream, cluster, a, ring);
 }
 
 }  // namespace

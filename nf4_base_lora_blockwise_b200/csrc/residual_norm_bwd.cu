@@ -23,37 +23,21 @@ struct BwdSlots {
 // br (w_post + o) S for a channel gate, both constant over m.  The CTA's sums go to `part` for
 // column_sum_kernel, which adds them in a fixed order: the results do not depend on timing.  In rows
 // that start inside a granule a thread's columns change from row to row: there each group adds to
-// sums in shared memory (of the widest rows, to the CTA's row of `part`), its rows kept apart by
-// its barrier.
-// T: threads at most; 512 leave the 128 registers that the sums and a row's data take.  WS: with the
-// weights staged; GF: with a whole gate.
-// One group's sums of columns, in rows that are not ALIGNED.
-struct ColumnSums {
-  float* shared;  // skewed, [2][ld]; or null
-  float* global;  // [2], `apart` apart
-  int64_t apart;
-  int ld, D;
-  __device__ __forceinline__ void add(int which, int at, int c, int shift, const f2 (&q)[4]) {
-    float f[8];
+// sums in shared memory, its rows kept apart by its barrier.
+// T = 512 threads leave the 128 registers that the sums and a row's data take.  WS: with the weights
+// staged; GF: with a whole gate.
+// Adds a vector to one group's sums of columns (skewed), in rows that are not ALIGNED.
+__device__ __forceinline__ void add_columns(float* sums, int at, int shift, const f2 (&q)[4]) {
+  float* p = sums + at - shift;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 t = split(q[k]);
-      f[2 * k] = t.x;
-      f[2 * k + 1] = t.y;
-    }
-    if (shared) {
-      float* p = shared + which * ld + at - shift;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) (k < shift ? p - 1 : p)[k] += f[k];
-    } else {
-      float* p = global + which * apart + c - shift;
-      for (int k = 0; k < 8; ++k)
-        if (c - shift + k >= 0 && c - shift + k < D) p[k] += f[k];
-    }
+  for (int k = 0; k < 4; ++k) {
+    const float2 t = split(q[k]);
+    (2 * k < shift ? p - 1 : p)[2 * k] += t.x;
+    (2 * k + 1 < shift ? p - 1 : p)[2 * k + 1] += t.y;
   }
-};
+}
 
-template <typename R, int T, bool ALIGNED, bool DW, bool WS, bool GF>
+template <typename R, int T, bool PAIR, bool ALIGNED, bool DW, bool WS, bool GF>
 __global__ void __launch_bounds__(T, 1)
     residual_norm_bwd_kernel(const __grid_constant__ ResidualNormBwd a,
                              const __grid_constant__ Ring ring) {
@@ -62,7 +46,7 @@ __global__ void __launch_bounds__(T, 1)
   extern __shared__ __align__(16) unsigned char smem_raw[];
   __shared__ __align__(16) float buf[4][kSumBuf];
   const uint32_t smem = smem_u32(smem_raw);
-  const Lane<NV> l = lane_of<NV, T, ALIGNED>(ring, smem, a.D);
+  const Lane<NV> l = lane_of<NV, T, ALIGNED, PAIR>(ring, smem, a.D);
   pdl_wait();  // the previous kernel's outputs are complete
   pdl_trigger();
   const float inv_d = 1.f / static_cast<float>(a.D);
@@ -86,11 +70,12 @@ __global__ void __launch_bounds__(T, 1)
 #pragma unroll
     for (int k = 0; k < 4; ++k) s_pre[j][k] = s_post[j][k] = both(0.f);
 
-  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;
+  const int64_t walker = PAIR ? blockIdx.x / 2 : blockIdx.x, walkers = PAIR ? gridDim.x / 2 : gridDim.x;
+  const int64_t step = walkers * blockDim.y;
   RowAt r, next;
   r.total = next.total = a.M * a.D;
   r.D = next.D = a.D;
-  int64_t m = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  int64_t m = walker * blockDim.y + threadIdx.y;
   advance(r, m, a.M);
   if constexpr (ALIGNED) clear_slots<NV, T>(ring, l, r);
   // Four copy groups a row, in the order of their use: dn, h', dh', then y and a whole gate.
@@ -115,25 +100,12 @@ __global__ void __launch_bounds__(T, 1)
   start_h(r);
   start_dh(r);
   start_y(r);
-  ColumnSums sums = {};
-  if constexpr (DW && !ALIGNED) {
-    sums.ld = ring.weights_ld;
-    sums.D = a.D;
-    sums.global = a.part + blockIdx.x * static_cast<int64_t>(a.part_ld);
-    sums.apart = gridDim.x * static_cast<int64_t>(a.part_ld);
-    const int tid = threadIdx.y * blockDim.x + threadIdx.x, threads = blockDim.x * blockDim.y;
-    if (ring.sums >= 0) {
-      float* all = reinterpret_cast<float*>(smem_raw + ring.sums);
-      sums.shared = all + threadIdx.y * 2 * sums.ld;
-      for (int i = tid; i < static_cast<int>(blockDim.y) * 2 * sums.ld; i += threads) all[i] = 0.f;
-    } else {
-      for (int i = tid; i < a.part_ld; i += threads)
-        sums.global[i] = sums.global[sums.apart + i] = 0.f;
-    }
-  }
-  if constexpr (WS) stage_weights<ALIGNED>(w, ring, smem_raw, wide);
+  float* sums = reinterpret_cast<float*>(smem_raw + ring.sums) + threadIdx.y * 2 * ring.weights_ld;
+  if constexpr (DW && !ALIGNED)
+    for (int i = threadIdx.x; i < 2 * ring.weights_ld; i += blockDim.x) sums[i] = 0.f;
+  if constexpr (WS) stage_weights<ALIGNED, PAIR>(w, ring, smem_raw, wide);
   clear_sums(buf, 4);
-  __syncthreads();
+  all_sync<PAIR>();
 
   // A row's scalars, read a round ahead: 1 / rms of h' and of y (1 without w_post; 0 without a
   // row), a token's gate or 1.
@@ -154,7 +126,7 @@ __global__ void __launch_bounds__(T, 1)
   // The same number of rounds for every group, so that a warp's slices stay together.  A round
   // without a row finds the last row's data (or zeros) and meets it with zero factors.
   int parity = 0;
-  for (int64_t base = static_cast<int64_t>(blockIdx.x) * blockDim.y; base < a.M; base += step) {
+  for (int64_t base = walker * blockDim.y; base < a.M; base += step) {
     advance(next, m + step, a.M);
     const Scalars then = scalars(next, m + step);
     f2 G[NV][4];
@@ -178,13 +150,12 @@ __global__ void __launch_bounds__(T, 1)
           if constexpr (DW && !ALIGNED) h[k] = mul2(p, rh2);
         }
         if constexpr (DW && !ALIGNED) {
-          if (a.dw_pre) sums.add(0, l.w[j], l.c[j], static_cast<int>(r.at & 7), h);
+          if (a.dw_pre) add_columns(sums, l.w[j], static_cast<int>(r.at & 7), h);
         }
       }
       start_dn(next);
-      float s[1] = {sum2(ss)};
-      row_sum<1>(s, buf[parity * 2]);
-      const f2 c2 = both(-s[0] * inv_d * rh * rh * rh);
+      const float s = row_sum<PAIR>(sum2(ss), buf[parity * 2]);
+      const f2 c2 = both(-s * inv_d * rh * rh * rh);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         f2 h[4];
@@ -262,20 +233,20 @@ __global__ void __launch_bounds__(T, 1)
           }
           if constexpr (DW && !ALIGNED) {
             if (a.dw_post || (a.dgate && gate_c))
-              sums.add(1, l.w[j], l.c[j], static_cast<int>(r.at & 7), y);
+              add_columns(sums + ring.weights_ld, l.w[j], static_cast<int>(r.at & 7), y);
           }
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) G[j][k] = t[k];
       }
-      float s[1] = {sum2(ss)};
+      float s = 0.f;
       if (post || token_sum) {
-        row_sum<1>(s, buf[parity * 2 + 1]);
-        if (token_sum && r.row && threadIdx.x == 0)
-          static_cast<float*>(a.dgate)[m] = a.branch_scale * ry * s[0];
+        s = row_sum<PAIR>(sum2(ss), buf[parity * 2 + 1]);
+        if (token_sum && r.row && l.c[0] == 0)
+          static_cast<float*>(a.dgate)[m] = a.branch_scale * ry * s;
       }
       const float brk = a.branch_scale * token;
-      const f2 ct = both(post ? brk * ry : brk), cy = both(-brk * ry * ry * ry * s[0] * inv_d);
+      const f2 ct = both(post ? brk * ry : brk), cy = both(-brk * ry * ry * ry * s * inv_d);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
 #pragma unroll
@@ -298,17 +269,26 @@ __global__ void __launch_bounds__(T, 1)
   }
 
   if constexpr (DW && !ALIGNED) {
-    if (!sums.shared) return;
-    __syncthreads();
+    all_sync<PAIR>();
     const float* all = reinterpret_cast<const float*>(smem_raw + ring.sums);
-    for (int c = threadIdx.y * blockDim.x + threadIdx.x; c < a.D; c += blockDim.x * blockDim.y) {
+    const int first = part_first<PAIR>(ring);
+    const int tid = threadIdx.y * blockDim.x + threadIdx.x, threads = blockDim.x * blockDim.y;
+    // The second CTA of a pair also met the first one's last columns.
+    const int rank = PAIR ? static_cast<int>(cluster_ctarank()) : 0;
+    const int end = PAIR && rank == 0 ? ring.width : a.D - first;
+    for (int c = tid; c < end; c += threads) {
       float s[2] = {0.f, 0.f};
       for (int y = 0; y < static_cast<int>(blockDim.y); ++y)
 #pragma unroll
-        for (int q = 0; q < 2; ++q) s[q] += all[(y * 2 + q) * sums.ld + skewed(c)];
-      sums.global[c] = s[0];
-      sums.global[sums.apart + c] = s[1];
+        for (int q = 0; q < 2; ++q) {
+          s[q] += all[(y * 2 + q) * ring.weights_ld + skewed(c)];
+          if (PAIR && rank == 0 && c >= end - 8)
+            s[q] += ld_peer(all + (y * 2 + q) * ring.weights_ld + skewed(c - end), 1);
+        }
+      a.part[walker * a.part_ld + first + c] = s[0];
+      a.part[(walkers + walker) * a.part_ld + first + c] = s[1];
     }
+    if constexpr (PAIR) cluster_sync_all();  // the peer has read
   }
   if constexpr (DW && ALIGNED) {
     // The CTA's row groups are added in order through the streams' memory (no copy is in flight: a
@@ -332,7 +312,7 @@ __global__ void __launch_bounds__(T, 1)
       for (int j = 0; j < NV; ++j) {
         const int c = l.c[j];
         if (c >= a.D) continue;
-        spill(groups + (threadIdx.y * 2) * ld + c, s_pre[j]);
+        spill(groups + (threadIdx.y * 2) * ld + c, s_pre[j]);  // (several groups: no pair)
         spill(groups + (threadIdx.y * 2 + 1) * ld + c, s_post[j]);
       }
       __syncthreads();
@@ -351,9 +331,8 @@ __global__ void __launch_bounds__(T, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) s_post[j][k] = add2(s_post[j][k], pair(t[2 * k], t[2 * k + 1]));
       }
-      const int64_t row = blockIdx.x;
-      if (a.dw_pre) spill(a.part + row * ld + c, s_pre[j]);
-      if (a.dw_post || (a.dgate && gate_c)) spill(a.part + (gridDim.x + row) * ld + c, s_post[j]);
+      if (a.dw_pre) spill(a.part + walker * ld + c, s_pre[j]);
+      if (a.dw_post || (a.dgate && gate_c)) spill(a.part + (walkers + walker) * ld + c, s_post[j]);
     }
   }
 }
@@ -402,50 +381,55 @@ __global__ void __launch_bounds__(32 * kSumLanes)
         a.w_post ? sum * (load_either1(a.w_post, a.weight_f32, c) + a.weight_offset) : sum;
 }
 
-RowShape bwd_shape(int64_t M, int D) {
-  return row_shape(M, D, D + (D % 8 ? 7 : 0) <= 8192 ? 512 : 1024);
-}
-
-template <typename R, int T, bool ALIGNED, bool DW, bool GF>
+template <typename R, int T, bool PAIR, bool ALIGNED, bool DW, bool GF>
 cudaError_t launch_bwd(const ResidualNormBwd& a, RowShape s, cudaStream_t st) {
   Ring ring = {};
   bool ws;
   const bool weights = a.w_pre || a.w_post || a.gate_kind == kGateChannel;
-  int smem = plan_ring(a.M, a.D, BwdSlots<R, 2>::GATE, GF, a.gate_f32, weights && T == 512, DW, s,
-                       &ring, &ws);
-  if (DW && !ALIGNED && ring.sums < 0 && s.rpc > 1) return cudaErrorInvalidConfiguration;
+  int smem = plan_ring(a.M, a.D, BwdSlots<R, 2>::GATE, GF, a.gate_f32, weights, DW, s, &ring, &ws);
+  if (DW && !ALIGNED && ring.sums < 0) return cudaErrorInvalidConfiguration;
   if (DW && ALIGNED && s.rpc > 1) {  // the row groups' sums go through the same memory
     const int sums = s.rpc * 2 * a.part_ld * static_cast<int>(sizeof(float));
     if (sums > smem) smem = sums;
   }
-  if constexpr (T == 512) {
-    if (ws)
-      return launch_rows(residual_norm_bwd_kernel<R, T, ALIGNED, DW, true, GF>, s, a, ring, smem,
-                         st);
-  }
-  return launch_rows(residual_norm_bwd_kernel<R, T, ALIGNED, DW, false, GF>, s, a, ring, smem, st);
+  return ws ? launch_rows(residual_norm_bwd_kernel<R, T, PAIR, ALIGNED, DW, true, GF>, s, a, ring,
+                          smem, st)
+            : launch_rows(residual_norm_bwd_kernel<R, T, PAIR, ALIGNED, DW, false, GF>, s, a, ring,
+                          smem, st);
 }
-template <typename R, int T, bool ALIGNED>
-cudaError_t launch_bwd(const ResidualNormBwd& a, const RowShape& s, bool dw, cudaStream_t st) {
-  if (a.gate_kind == kGateFull)
-    return dw ? launch_bwd<R, T, ALIGNED, true, true>(a, s, st)
-              : launch_bwd<R, T, ALIGNED, false, true>(a, s, st);
-  return dw ? launch_bwd<R, T, ALIGNED, true, false>(a, s, st)
-            : launch_bwd<R, T, ALIGNED, false, false>(a, s, st);
+template <typename R, int T, bool PAIR, bool ALIGNED, bool DW>
+cudaError_t launch_bwd(const ResidualNormBwd& a, const RowShape& s, cudaStream_t st) {
+  return a.gate_kind == kGateFull ? launch_bwd<R, T, PAIR, ALIGNED, DW, true>(a, s, st)
+                                  : launch_bwd<R, T, PAIR, ALIGNED, DW, false>(a, s, st);
 }
 template <typename R>
 cudaError_t launch_bwd(const ResidualNormBwd& a, const RowShape& s, bool dw, cudaStream_t st) {
-  if (s.threads == 512)
-    return s.aligned ? launch_bwd<R, 512, true>(a, s, dw, st)
-                     : launch_bwd<R, 512, false>(a, s, dw, st);
-  return s.aligned ? launch_bwd<R, 1024, true>(a, s, dw, st)
-                   : launch_bwd<R, 1024, false>(a, s, dw, st);
+  if (s.threads == 1024) return launch_bwd<R, 1024, false, true, false>(a, s, st);
+  if (s.pair) {
+    if (!s.aligned)
+      return dw ? launch_bwd<R, 512, true, false, true>(a, s, st)
+                : launch_bwd<R, 512, true, false, false>(a, s, st);
+    return launch_bwd<R, 512, true, true, true>(a, s, st);
+  }
+  if (s.aligned)
+    return dw ? launch_bwd<R, 512, false, true, true>(a, s, st)
+              : launch_bwd<R, 512, false, true, false>(a, s, st);
+  return dw ? launch_bwd<R, 512, false, false, true>(a, s, st)
+            : launch_bwd<R, 512, false, false, false>(a, s, st);
+}
+
+// Up to 8192 columns (or the granules of as many) 512 threads take a row; then 1024 without column
+// sums in rows of whole granules, else a pair of 512.
+RowShape bwd_shape(int64_t M, int D, bool dw) {
+  const bool wide = D + (D % 8 ? 7 : 0) > 8192;
+  const bool one = wide && D % 8 == 0 && !dw;
+  return row_shape(M, D, one ? 1024 : 512, wide && !one);
 }
 
 }  // namespace
 
 size_t residual_norm_part_bytes(int64_t M, int D) {
-  return static_cast<size_t>(2 * bwd_shape(M, D).ctas) * ((D + 7) / 8 * 8) * sizeof(float);
+  return static_cast<size_t>(2 * bwd_shape(M, D, true).walkers) * ((D + 7) / 8 * 8) * sizeof(float);
 }
 
 cudaError_t launch_residual_norm_bwd(const ResidualNormBwd& args, cudaStream_t stream, int* n) {
@@ -453,16 +437,16 @@ cudaError_t launch_residual_norm_bwd(const ResidualNormBwd& args, cudaStream_t s
   a.part_ld = (a.D + 7) / 8 * 8;
   const bool second = a.dw_post || (a.dgate && a.gate_kind == kGateChannel);
   const bool dw = a.dw_pre || second;
-  const RowShape s = bwd_shape(a.M, a.D);
+  const RowShape s = bwd_shape(a.M, a.D, dw);
   const cudaError_t e = a.resid_f32 ? launch_bwd<float>(a, s, dw, stream)
                                     : launch_bwd<__nv_bfloat16>(a, s, dw, stream);
   *n = 1;
   if (e != cudaSuccess || !dw) return e;
   *n = 2;
   int lanes = 1;
-  while (lanes < kSumLanes && lanes * 8 < s.ctas) lanes *= 2;
+  while (lanes < kSumLanes && lanes * 8 < s.walkers) lanes *= 2;
   return launch_pdl(column_sum_kernel, dim3((a.D + 31) / 32, second ? 2 : 1), dim3(32, lanes), 0,
-                    stream, 1, a.part, static_cast<int>(s.ctas), a);
+                    stream, 1, a.part, static_cast<int>(s.walkers), a);
 }
 
 }  // namespace qlora
