@@ -102,6 +102,13 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
+// a + b, where a and b may be products: a packed multiplication and addition are contracted into a
+// fused one in spite of their rounding modifiers, the scalar intrinsic is not.
+__device__ __forceinline__ f2 add2_unfused(f2 a, f2 b) {
+  const float2 x = split(a), y = split(b);
+  return pair(__fadd_rn(x.x, y.x), __fadd_rn(x.y, y.y));
+}
+
 // Square roots of two numbers in [kRootLow, kRootHigh], correctly rounded: the approximate
 // reciprocal root r, s = v r, and Markstein's correction s + (v - s^2) r / 2 with a fused residual
 // ("IA-64 and Elementary Functions", square root), which leaves a relative 2^-45 before the last
@@ -218,11 +225,11 @@ __global__ void __launch_bounds__(kAdamThreads)
   if (threadIdx.x == 0) {
     t = 0.0;
     for (int i = 0; i < kAdamWarps; ++i) t += s[i];
-    const double norm = sqrt(t) * fabs(static_cast<double>(a.grad_scale));
+    const double norm = sqrt(t) * fabs(a.grad_scale);
     double clip = 1.0;
-    if (a.max_norm > 0.f) clip = fmin(1.0, static_cast<double>(a.max_norm) / (norm + 1e-6));
+    if (a.max_norm > 0.0) clip = fmin(1.0, a.max_norm / (norm + 1e-6));
     st->norm = static_cast<float>(norm);
-    st->factor = static_cast<float>(static_cast<double>(a.grad_scale) * clip);
+    st->factor = static_cast<float>(a.grad_scale * clip);
     const int ok = isfinite(norm);
     st->finite = ok;
     if (!ok) st->skipped += 1;
@@ -301,7 +308,7 @@ __global__ void __launch_bounds__(kAdamThreads, 4)
   }
   __syncthreads();
   const float c1 = sc[0];
-  const float factor = a.use_norm ? st->factor : a.grad_scale;
+  const float factor = a.use_norm ? st->factor : static_cast<float>(a.grad_scale);
   const float lr = a.lr_dev ? *a.lr_dev : a.lr;
   const uint32_t word = mix32(mix32(a.seed) + static_cast<uint32_t>(step_s));
   const f2 c2 = both(sc[1]), eps = both(a.eps), fac = both(factor);
@@ -327,8 +334,8 @@ __global__ void __launch_bounds__(kAdamThreads, 4)
         mk = h.m[k];
         vk = h.v[k];
       }
-      m2[k] = add2(mul2(mk, both(a.b1)), mul2(g, both(a.one_b1)));
-      v2[k] = add2(mul2(vk, both(a.b2)), mul2(mul2(g, g), both(a.one_b2)));
+      m2[k] = add2_unfused(mul2(mk, both(a.b1)), mul2(g, both(a.one_b1)));
+      v2[k] = add2_unfused(mul2(vk, both(a.b2)), mul2(mul2(g, g), both(a.one_b2)));
       const float2 v = split(v2[k]);
       vmax = k == 0 ? max_nan(v.x, v.y) : max_nan(vmax, max_nan(v.x, v.y));
       vmin = k == 0 ? fminf(v.x, v.y) : fminf(vmin, fminf(v.x, v.y));

@@ -472,8 +472,8 @@ struct AdamArgs {
   int part_first;        // this launch's first
   int part_count;        // of the whole list
   const float* lr_dev;   // or null: lr
-  float lr, b1, b2, one_b1, one_b2, eps, grad_scale, max_norm;
-  double b1d, b2d;
+  float lr, b1, b2, one_b1, one_b2, eps;
+  double b1d, b2d, grad_scale, max_norm;
   uint32_t seed;
   bool bits8, use_norm, last;  // last: the launch that closes the step
 };

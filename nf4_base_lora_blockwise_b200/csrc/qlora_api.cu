@@ -1598,8 +1598,8 @@ qlora_status qlora_adamw_step(const qlora_adamw_tensor* tensors, int count_,
   a.one_b1 = static_cast<float>(1.0 - c.beta1);
   a.one_b2 = static_cast<float>(1.0 - c.beta2);
   a.eps = static_cast<float>(c.eps);
-  a.grad_scale = static_cast<float>(c.grad_scale);
-  a.max_norm = static_cast<float>(c.max_norm);
+  a.grad_scale = c.grad_scale;
+  a.max_norm = c.max_norm;
   a.b1d = c.beta1;
   a.b2d = c.beta2;
   a.seed = c.seed;

@@ -295,6 +295,25 @@ def test_learning_rate_on_the_device_and_assigned():
     assert float(a.lr) == 0.0 and b.lr == 0.0
 
 
+def test_moments_are_separately_rounded():
+    """The fp32 moments are products and sums rounded one by one, to the bit: what 8-bit codes are
+    decided from."""
+    n = 100_000
+    g = torch.Generator(device="cuda").manual_seed(1)
+    grad = torch.randn(n, generator=g, device="cuda")
+    opt = optim.AdamW([torch.zeros(n, device="cuda")], [grad], betas=(0.9, 0.999),
+                      max_grad_norm=0.3)
+    m = v = torch.zeros(n, device="cuda")
+    for _ in range(3):
+        opt.step()
+        norm = grad.double().square().sum().sqrt()
+        part = grad * torch.clamp(0.3 / (norm + 1e-6), max=1.0).float()
+        m = m * 0.9 + part * (1 - 0.9)
+        v = v * 0.999 + part * part * (1 - 0.999)
+        assert torch.equal(opt.m[:n], m) and torch.equal(opt.v[:n], v)
+        grad.mul_(-0.7)
+
+
 def test_square_roots_are_the_nearest():
     """Every mantissa under both parities of the exponent, at 1, and near both ends of the range."""
     from nf4_base_lora_blockwise_b200 import abi
