@@ -171,13 +171,13 @@ __device__ __forceinline__ void corrections(const AdamArgs& a, int64_t t, float*
   *c2 = static_cast<float>(1.0 / sqrt(1.0 - power(a.b2d, t)));
 }
 
-// Sums of squares of the scaled gradients, in 64 bits (no overflow for finite gradients), one a
-// CTA; the last CTA of the list adds them in order and leaves norm and factor in the state.
+// Sums of squares of the gradients, in 64 bits (no overflow for finite gradients), one a CTA.  Each
+// CTA of the step adds them up, in the same order, instead of a last CTA here: that one would wait
+// for a fence, a ticket and the other sums, and the step for it.
 template <int N>
 __global__ void __launch_bounds__(kAdamThreads)
     adam_norm_kernel(const __grid_constant__ AdamTable<N> table, const AdamArgs a) {
   __shared__ double s[kAdamWarps];
-  __shared__ bool last;
   pdl_wait();  // the previous kernel's outputs are complete
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -202,39 +202,10 @@ __global__ void __launch_bounds__(kAdamThreads)
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
   if (lane == 0) s[warp] = sum;
   __syncthreads();
-  AdamState* st = static_cast<AdamState*>(a.state);
   if (threadIdx.x == 0) {
     double t = 0.0;
     for (int i = 0; i < kAdamWarps; ++i) t += s[i];
     a.part[a.part_first + blockIdx.x] = t;
-    last = false;
-    if (a.last) {
-      __threadfence();
-      last = atomicAdd(&st->ticket, 1u) == gridDim.x - 1;
-    }
-  }
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  double t = 0.0;
-  for (int i = threadIdx.x; i < a.part_count; i += kAdamThreads) t += __ldcg(a.part + i);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
-  if (lane == 0) s[warp] = t;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    t = 0.0;
-    for (int i = 0; i < kAdamWarps; ++i) t += s[i];
-    const double norm = sqrt(t) * fabs(a.grad_scale);
-    double clip = 1.0;
-    if (a.max_norm > 0.0) clip = fmin(1.0, a.max_norm / (norm + 1e-6));
-    st->norm = static_cast<float>(norm);
-    st->factor = static_cast<float>(a.grad_scale * clip);
-    const int ok = isfinite(norm);
-    st->finite = ok;
-    if (!ok) st->skipped += 1;
-    corrections(a, st->step + 1, &st->c1, &st->c2);
-    st->ticket = 0;
   }
 }
 
@@ -280,13 +251,15 @@ __global__ void __launch_bounds__(kAdamThreads, 4)
     adam_step_kernel(const __grid_constant__ AdamTable<N> table,
                      const __grid_constant__ AdamArgs a) {
   __shared__ float sc[2];
+  __shared__ double parts[kAdamWarps];
   __shared__ int64_t step_s;
   __shared__ CodeTables codes;
   if constexpr (BITS8) fill_tables(codes);
-  pdl_wait();  // the previous kernel's outputs are complete
-  pdl_trigger();
+  // A norm kernel in front has waited for what precedes it before it let this one start, and
+  // writes no tensor: only its sums have to be waited for, after the first loads and the
+  // corrections.
+  if (!a.use_norm) pdl_wait();
   AdamState* st = static_cast<AdamState*>(a.state);
-  if (a.use_norm && !st->finite) return;  // the whole step is left out
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t end = share(a.blocks, blockIdx.x + 1);
   uint32_t b = share(a.blocks, blockIdx.x) + warp;
@@ -297,18 +270,35 @@ __global__ void __launch_bounds__(kAdamThreads, 4)
     load_block(table.t[ti], a, b, lane, h);
   }
   if (threadIdx.x == 0) {
-    const int64_t t = st->step + 1;
-    step_s = t;
-    if (a.use_norm) {
-      sc[0] = st->c1;
-      sc[1] = st->c2;
-    } else {
-      corrections(a, t, &sc[0], &sc[1]);
-    }
+    step_s = st->step + 1;
+    corrections(a, step_s, &sc[0], &sc[1]);
+  }
+  float factor = static_cast<float>(a.grad_scale);
+  if (a.use_norm) {
+    pdl_wait();
+    double t = 0.0;
+    for (int i = threadIdx.x; i < a.part_count; i += kAdamThreads) t += __ldcg(a.part + i);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+    if (lane == 0) parts[warp] = t;
   }
   __syncthreads();
+  pdl_trigger();
+  if (a.use_norm) {
+    double t = 0.0;
+#pragma unroll
+    for (int i = 0; i < kAdamWarps; ++i) t += parts[i];
+    const double norm = sqrt(t) * fabs(a.grad_scale);
+    if (a.max_norm > 0.0)
+      factor = static_cast<float>(a.grad_scale * fmin(1.0, a.max_norm / (norm + 1e-6)));
+    const bool ok = isfinite(norm);
+    if (a.last && blockIdx.x == 0 && threadIdx.x == 0) {
+      st->norm = static_cast<float>(norm);
+      st->skipped += !ok;
+    }
+    if (!ok) return;  // the whole step is left out
+  }
   const float c1 = sc[0];
-  const float factor = a.use_norm ? st->factor : static_cast<float>(a.grad_scale);
   const float lr = a.lr_dev ? *a.lr_dev : a.lr;
   const uint32_t word = mix32(mix32(a.seed) + static_cast<uint32_t>(step_s));
   const f2 c2 = both(sc[1]), eps = both(a.eps), fac = both(factor);

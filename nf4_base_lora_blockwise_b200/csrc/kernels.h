@@ -480,12 +480,10 @@ struct AdamArgs {
 struct AdamState {       // device, zero (or the steps taken so far) before the first step
   int64_t step;          // steps taken
   float norm;            // of the last step's gradients, scaled
-  float factor;          // on the gradients of the last step
+  int32_t unused;
   int32_t skipped;       // steps left out for a norm that was not finite
   uint32_t ticket;       // zero between launches
-  int32_t finite;
-  float c1, c2;          // 1 / (1 - b1^t), 1 / sqrt(1 - b2^t) of the next step
-  int32_t pad[7];
+  int32_t pad[10];
 };
 constexpr int kAdamNormCtas = 148 * 8;  // at most: one double of workspace each
 int adam_norm_ctas(uint32_t blocks);

@@ -1610,7 +1610,8 @@ qlora_status qlora_adamw_step(const qlora_adamw_tensor* tensors, int count_,
   // Launches of up to kAdamTensors tensors: first every launch's norm, then every launch's step.
   for (int pass = use_norm ? 0 : 1; pass < 2; ++pass) {
     int64_t first = 0;
-    int part = 0;
+    a.part_count = a.part_first;  // of the norm's launches
+    a.part_first = 0;
     for (int i = 0; i < count_; i += kAdamTensors) {
       AdamTensor table[kAdamTensors];
       a.tensors = 0;
@@ -1634,13 +1635,11 @@ qlora_status qlora_adamw_step(const qlora_adamw_tensor* tensors, int count_,
       a.blocks = static_cast<uint32_t>(blocks);
       a.first_block = first;
       a.last = end == count_;
-      a.part_first = part;
-      part += adam_norm_ctas(a.blocks);
-      a.part_count = part;
       st = cuda_status(pass == 0 ? launch_adam_norm(table, a, s) : launch_adam_step(table, a, s));
       if (st != QLORA_OK) return st;
       count(1);
       first += blocks;
+      a.part_first += adam_norm_ctas(a.blocks);
     }
   }
   return QLORA_OK;
