@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(T, 1)
   Scalars now = scalars(r, m);
 
   // The same number of rounds for every group, so that a warp's slices stay together.  A round
-  // without a row finds the last row's data (or zeros) and meets it with zero factors.
+  // without a row finds zeros, and zero factors.
   int parity = 0;
   for (int64_t base = walker * blockDim.y; base < a.M; base += step) {
     advance(next, m + step, a.M);
@@ -261,6 +261,13 @@ __global__ void __launch_bounds__(T, 1)
       }
     }
     start_y(next);
+    if constexpr (ALIGNED) {
+      // A last round without a row: the zero factors would make NaN of an infinity left here.
+      if (r.row && !next.row) {
+        wait_copies<0>();
+        clear_slots<NV, T>(ring, l, next);
+      }
+    }
     if constexpr (DW && !ALIGNED) group_sync();  // the next row's sums follow this one's
     r = next;
     now = then;

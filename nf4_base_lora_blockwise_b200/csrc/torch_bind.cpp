@@ -116,6 +116,39 @@ qlora_stream_t stream(int dev) {
       c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream());
 }
 
+// The bytes of a contiguous tensor, empty for none.
+std::pair<uintptr_t, uintptr_t> span(const Tensor* t) {
+  if (!t || !t->defined()) return {0, 0};
+  const auto p = reinterpret_cast<uintptr_t>(t->const_data_ptr());
+  return {p, p + t->nbytes()};
+}
+// Given outputs share no memory with the inputs or with each other, but as a pair of `same` says
+// {output, input}: those may start at the same address.
+struct Named {
+  const char* name;
+  const Tensor* t;
+};
+void apart(at::ArrayRef<Named> outs, at::ArrayRef<Named> ins,
+           at::ArrayRef<std::pair<const Tensor*, const Tensor*>> same) {
+  auto meet = [](const Tensor* a, const Tensor* b) {
+    const auto x = span(a), y = span(b);
+    return x.first < y.second && y.first < x.second;
+  };
+  for (size_t i = 0; i < outs.size(); ++i) {
+    const Tensor* o = outs[i].t;
+    if (!o) continue;
+    for (const Named& in : ins)
+      if (meet(o, in.t)) {
+        bool allowed = false;
+        for (const auto& [a, b] : same)
+          allowed |= a == o && b == in.t && span(a) == span(b);
+        TORCH_CHECK_VALUE(allowed, outs[i].name, ": shares memory with ", in.name);
+      }
+    for (size_t j = 0; j < i; ++j)
+      TORCH_CHECK_VALUE(!meet(o, outs[j].t), outs[i].name, ": shares memory with ", outs[j].name);
+  }
+}
+
 // New references into a tuple; undefined tensors as None, a given tensor as the object it came as.
 PyObject* object(const Tensor& t, PyObject* given) {
   if (given && given != Py_None) return Py_NewRef(given);
@@ -197,6 +230,10 @@ PyObject* residual_norm_forward(PyObject*, PyObject* const* a, Py_ssize_t na) {
     TORCH_CHECK_VALUE(!given_post, "residual_norm_forward: rstd_post needs w_post");
   }
   TORCH_CHECK_VALUE(D <= INT32_MAX, "h: too wide");
+  if (given_h || given_n || given_pre || given_post)
+    apart({{"h_out", given_h}, {"n", given_n}, {"rstd_pre", given_pre}, {"rstd_post", given_post}},
+          {{"h", &h}, {"y", y}, {"w_pre", w.w_pre}, {"w_post", w.w_post}, {"gate", w.gate}},
+          {{given_h, &h}, {given_n, y}});
   if (M > 0 &&
       failed("qlora_residual_norm_fwd",
              qlora_residual_norm_fwd(ptr(h), ptr(y), ptr(w.w_pre), ptr(w.w_post), ptr(w.gate),
@@ -268,6 +305,17 @@ PyObject* residual_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t na) {
     dgate = w.kind == QLORA_GATE_CHANNEL ? out(g, {D}, kF32, "dgate", dev)
             : w.kind == QLORA_GATE_TOKEN ? out(g, {M, 1}, kF32, "dgate", dev)
                                          : out(g, {M, D}, w.gate->scalar_type(), "dgate", dev);
+  }
+  bool given = false;
+  for (int i = 15; i < 21; ++i) given |= a[i] != Py_None;
+  if (given) {
+    auto of = [&](int i, const Tensor& used) { return used.defined() ? opt(a[i], "") : nullptr; };
+    const Tensor *gh = of(15, dh), *gy = of(16, dy);
+    apart({{"dh", gh}, {"dy", gy}, {"dw_pre", of(17, dw_pre)}, {"dw_post", of(18, dw_post)},
+           {"dgate", of(19, dgate)}, {"ws", opt(a[20], "ws")}},
+          {{"dn", dn}, {"dh_out", dh_out}, {"h_out", h_out}, {"y", y}, {"rstd_pre", rstd_pre},
+           {"rstd_post", rstd_post}, {"w_pre", w.w_pre}, {"w_post", w.w_post}, {"gate", w.gate}},
+          {{gh, dh_out}, {gy, y}, {gy, dn}});
   }
   size_t ws_bytes = 0;
   if (dw_pre.defined() || dw_post.defined() ||
@@ -352,6 +400,32 @@ bool distinct(const Heads& h, int64_t hd) {
   return true;
 }
 
+// The distance from the first element of the heads to behind the last.
+int64_t reach(const Heads& h, int64_t hd) {
+  return h.B && h.S ? (h.B - 1) * h.batch + (h.S - 1) * h.token + (h.n - 1) * h.head + hd : 0;
+}
+// Whether two tensors of heads share no element: apart altogether, or in different parts of one of
+// the strides (such as of a packed row), of which all strides that reach further are multiples.
+bool apart(const Tensor& x, const Heads& a, const Tensor& y, const Heads& b, int64_t hd) {
+  const auto e = static_cast<int64_t>(x.element_size());
+  const auto p = reinterpret_cast<intptr_t>(x.const_data_ptr()),
+             q = reinterpret_cast<intptr_t>(y.const_data_ptr());
+  if (p + reach(a, hd) * e <= q || q + reach(b, hd) * e <= p) return true;
+  for (const int64_t s : {a.head, a.token, a.batch}) {
+    if (s < 1) continue;
+    auto part = [&](const Heads& h) {
+      int64_t r = hd;
+      if (h.B > 1 && h.batch % s) r += (h.B - 1) * h.batch;
+      if (h.S > 1 && h.token % s) r += (h.S - 1) * h.token;
+      if (h.n > 1 && h.head % s) r += (h.n - 1) * h.head;
+      return r * e;
+    };
+    const int64_t d = ((q - p) % (s * e) + s * e) % (s * e);
+    if (d >= part(a) && d + part(b) <= s * e) return true;
+  }
+  return false;
+}
+
 // (x, positions, phase, scale, head_dim, rotary_dim, interleaved, n_heads, k, n_heads_k, inverse,
 //  inplace, out, out_k)
 PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t na) {
@@ -363,6 +437,8 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t na) {
   const Tensor& phase = need(a[2], "plan.phase");
   const int64_t hd = integer(a[4]), rd = integer(a[5]);
   const auto type = x.scalar_type();
+  TORCH_CHECK_VALUE(hd >= 2 && rd >= 2 && rd <= hd, "plan: a head of ", hd, " with ", rd,
+                    " rotary elements");
   TORCH_CHECK_VALUE(either(type), "x: expected bf16 or fp32, got ", type);
   auto heads_arg = [](PyObject* o) { return o == Py_None ? int64_t{-1} : integer(o); };
   if (a[7] != Py_None)
@@ -379,6 +455,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t na) {
   static const char* out_names[2] = {"out", "out_k"};
   qlora_rope_heads q[2];
   Tensor outs[2];
+  Heads from[2], to[2];
   int64_t B = 0, S = 0;
   for (int i = 0; i < (k ? 2 : 1); ++i) {
     const Tensor& t = *in[i];
@@ -416,8 +493,26 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t na) {
     TORCH_CHECK_VALUE(distinct(o, hd), "rope: elements of ", inplace ? names[i] : out_names[i],
                       " share an address");
     TORCH_CHECK_VALUE(h.n <= INT32_MAX, names[i], ": too many heads");
+    from[i] = h;
+    to[i] = o;
     q[i] = {ptr(t),   ptr(outs[i]), h.batch, h.token, h.head,
             o.batch, o.token,      o.head,  static_cast<int>(h.n)};
+  }
+  // What is written shares no element with anything else: in place x with k, otherwise given
+  // outputs with the inputs (but one with its own, which is in place too) and each other.
+  if (inplace) {
+    if (k) TORCH_CHECK_VALUE(apart(x, from[0], *k, from[1], hd), "rope: x and k share elements");
+  } else if (given[0] || given[1]) {
+    for (int i = 0; i < (k ? 2 : 1); ++i)
+      for (int j = 0; given[i] && j < (k ? 2 : 1); ++j) {
+        const bool own = i == j && q[i].x == q[i].out && from[i].batch == to[i].batch &&
+                         from[i].token == to[i].token && from[i].head == to[i].head;
+        TORCH_CHECK_VALUE(own || apart(outs[i], to[i], *in[j], from[j], hd), out_names[i],
+                          ": shares elements with ", names[j]);
+      }
+    if (k)
+      TORCH_CHECK_VALUE(apart(outs[0], to[0], outs[1], to[1], hd),
+                        "rope: out and out_k share elements");
   }
   const void* pos = nullptr;
   bool pos64 = false;

@@ -277,3 +277,41 @@ def test_refusals():
                dict(ws=torch.empty(256, dtype=torch.uint8, device="cuda"))):
         with pytest.raises((ValueError, RuntimeError)):
             g(**kw)
+
+
+@pytest.mark.parametrize("M", [1, 2, 149, 300, 1500])
+@pytest.mark.parametrize("D", [64, 250, 2048])
+def test_an_infinity_stays_where_it_is(M, D):
+    """dn of one element infinite: its column's sum is, the others' are finite, also where rows do not
+    fill the last round."""
+    g = torch.Generator().manual_seed(1)
+    h = torch.randn(M, D, generator=g).abs().add(0.5).to(BF16).cuda()
+    w = torch.ones(D, dtype=BF16, device="cuda")
+    _, _, r, _ = block.residual_norm_forward(h, w_pre=w)
+    for row in {0, M // 2, M - 1}:
+        dn = torch.randn(M, D, generator=g).to(BF16).cuda()
+        dn[row, 5] = float("inf")
+        dh, _, dw, _, _ = block.residual_norm_backward(dn, None, h, rstd_pre=r, w_pre=w)
+        assert dw[5] == float("inf") and torch.isfinite(dw).sum() == D - 1
+        assert torch.isfinite(dh).all(1).sum() == M - 1
+
+
+def test_given_outputs_are_apart():
+    i = _inputs(8, 64, BF16, BF16, True, "channel", True, 1)
+    buf = torch.empty(3, 8, 64, dtype=BF16, device="cuda")
+    f = lambda **kw: block.residual_norm_forward(**{**dict(  # noqa: E731
+        h=i["h"], y=i["y"], w_pre=i["w_pre"], w_post=i["w_post"], gate=i["gate"]), **kw})
+    half = torch.empty(12, 64, dtype=BF16, device="cuda")
+    for kw in (dict(h_out=i["y"]), dict(n=i["h"]), dict(h_out=buf[0], n=buf[0]),
+               dict(h=half[:8], h_out=half[4:]), dict(n=half[:8], y=half[4:])):
+        with pytest.raises(ValueError, match="shares memory"):
+            f(**kw)
+    h, n, a, b = f()
+    g = lambda **kw: block.residual_norm_backward(**{**dict(  # noqa: E731
+        dn=i["dn"], dh_out=i["dh"], h_out=h, y=i["y"], rstd_pre=a, rstd_post=b, w_pre=i["w_pre"],
+        w_post=i["w_post"], gate=i["gate"]), **kw})
+    col = torch.empty(64, device="cuda")
+    for kw in (dict(dh=h), dict(dy=h), dict(dh=i["dn"]), dict(dh=buf[0], dy=buf[0]),
+               dict(dw_pre=col, dw_post=col), dict(dw_pre=col, dgate=col)):
+        with pytest.raises(ValueError, match="shares memory"):
+            g(**kw)

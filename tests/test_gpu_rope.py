@@ -189,3 +189,32 @@ def test_refusals():
     out = block.rope(row.expand(4, 256), pos, plan, inplace=False)
     _agree(out.view(4, 4, 64), row.expand(4, 256).view(4, 4, 64), pos.tolist(), plan, 10000.0, None,
            False)
+
+
+def test_what_is_written_is_apart():
+    """q and k of one packed row or cache are; the same heads twice, or an output over its input, not."""
+    plan = block.rope_plan(64)
+    row = _rnd(2, 6, 8 * 64)
+    want = block.rope(row.view(12, 512), 3, plan, n_heads=6, inplace=False)
+    for parts in (lambda t: (t[..., :256], t[..., 256:384]), lambda t: (t[..., 256:384], t[..., :256])):
+        r = row.clone().view(12, 512)
+        q, k = parts(r)
+        block.rope(q, 3, plan, k=k)
+        assert torch.equal(r[:, :384], want) and torch.equal(r[:, 384:], row.view(12, 512)[:, 384:])
+    cache = _rnd(2, 5, 6, 64)                                # [B, heads, S, 64]: heads further apart
+    c = cache.clone().transpose(1, 2)
+    block.rope(c[:, :, :3], 0, plan, k=c[:, :, 3:])
+    assert torch.equal(c, block.rope(cache.transpose(1, 2), 0, plan, inplace=False))
+    x, wide = _rnd(4, 256), _rnd(4, 320)
+    same = x.clone()
+    block.rope(same, 0, plan, out=same)                      # in place by name
+    assert torch.equal(same, block.rope(x, 0, plan, inplace=False))
+    y = _rnd(4, 256)
+    for kw in (dict(k=x), dict(k=x[:, 64:]), dict(k=x[1:2].expand(4, 256)), dict(x=wide[:, :256], out=wide[:, 64:]),
+               dict(k=y, out=y), dict(k=y, out=torch.empty_like(x), out_k=x),
+               dict(k=y, out=wide[:, :256], out_k=wide[:, 64:])):
+        with pytest.raises(ValueError, match="share"):
+            block.rope(**{**dict(x=x, positions=0, plan=plan), **kw})
+    for hd, rd in ((0, 0), (64, 0), (32, 64)):
+        with pytest.raises(ValueError):
+            block.rope(x, 0, block.RopePlan(plan.phase[:rd // 2], 1.0, hd, rd))
