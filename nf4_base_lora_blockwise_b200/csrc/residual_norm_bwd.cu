@@ -18,14 +18,6 @@ struct BwdSlots {
   static constexpr int DN = 0, H = NV, DH = H + NV * GR, Y = DH + NV * GR, GATE = Y + NV;
 };
 
-// DW: with the weights' and the channel gate's gradients.  Each thread sums its own columns over
-// its group's rows in registers: dw_pre, and S, from which dw_post = br gate S and dgate =
-// br (w_post + o) S for a channel gate, both constant over m.  The CTA's sums go to `part` for
-// column_sum_kernel, which adds them in a fixed order: the results do not depend on timing.  In rows
-// that start inside a granule a thread's columns change from row to row: there each group adds to
-// sums in shared memory, its rows kept apart by its barrier.
-// T = 512 threads leave the 128 registers that the sums and a row's data take.  WS: with the weights
-// staged; GF: with a whole gate.
 // Adds a vector to one group's sums of columns (skewed), in rows that are not ALIGNED.
 __device__ __forceinline__ void add_columns(float* sums, int at, int shift, const f2 (&q)[4]) {
   float* p = sums + at - shift;
@@ -37,7 +29,15 @@ __device__ __forceinline__ void add_columns(float* sums, int at, int shift, cons
   }
 }
 
-template <typename R, int T, bool PAIR, bool ALIGNED, bool DW, bool WS, bool GF>
+// DW: with the weights' and the channel gate's gradients.  Each thread sums its own columns over
+// its group's rows in registers: dw_pre, and S, from which dw_post = br gate S and dgate =
+// br (w_post + o) S for a channel gate, both constant over m.  The CTA's sums go to `part` for
+// column_sum_kernel, which adds them in a fixed order: the results do not depend on timing.  In rows
+// that start inside a granule a thread's columns change from row to row: there each group adds to
+// sums in shared memory, its rows kept apart by its barrier.
+// T = 512 threads leave the 128 registers that the sums and a row's data take.  WS: with the weights
+// staged; GF: with a whole gate; AHEAD: rows that are on their way beside the current one.
+template <typename R, int T, bool PAIR, bool ALIGNED, bool DW, bool WS, bool GF, int AHEAD>
 __global__ void __launch_bounds__(T, 1)
     residual_norm_bwd_kernel(const __grid_constant__ ResidualNormBwd a,
                              const __grid_constant__ Ring ring) {
@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(T, 1)
   extern __shared__ __align__(16) unsigned char smem_raw[];
   __shared__ __align__(16) float buf[4][kSumBuf];
   const uint32_t smem = smem_u32(smem_raw);
-  const Lane<NV> l = lane_of<NV, T, ALIGNED, PAIR>(ring, smem, a.D);
+  Lane<NV> l = lane_of<NV, T, ALIGNED, PAIR>(ring, smem, a.D);
   pdl_wait();  // the previous kernel's outputs are complete
   pdl_trigger();
   const float inv_d = 1.f / static_cast<float>(a.D);
@@ -77,6 +77,9 @@ __global__ void __launch_bounds__(T, 1)
   r.D = next.D = a.D;
   int64_t m = walker * blockDim.y + threadIdx.y;
   advance(r, m, a.M);
+  constexpr int MORE = 4 * (AHEAD - 1);  // copy groups in flight of the row after the next
+  const uint32_t turn = AHEAD == 2 ? l.slots ^ (l.slots + T * ring.slots * 16) : 0;
+  auto other = [&] { l.slots ^= turn; };  // two sets of slots take turns
   if constexpr (ALIGNED) clear_slots<NV, T>(ring, l, r);
   // Four copy groups a row, in the order of their use: dn, h', dh', then y and a whole gate.
   auto start_dn = [&](const RowAt& q) {
@@ -100,6 +103,16 @@ __global__ void __launch_bounds__(T, 1)
   start_h(r);
   start_dh(r);
   start_y(r);
+  if constexpr (AHEAD == 2) {
+    other();
+    advance(next, m + step, a.M);
+    clear_slots<NV, T>(ring, l, next);
+    start_dn(next);
+    start_h(next);
+    start_dh(next);
+    start_y(next);
+    other();
+  }
   float* sums = reinterpret_cast<float*>(smem_raw + ring.sums) + threadIdx.y * 2 * ring.weights_ld;
   if constexpr (DW && !ALIGNED)
     for (int i = threadIdx.x; i < 2 * ring.weights_ld; i += blockDim.x) sums[i] = 0.f;
@@ -129,12 +142,13 @@ __global__ void __launch_bounds__(T, 1)
   for (int64_t base = walker * blockDim.y; base < a.M; base += step) {
     advance(next, m + step, a.M);
     const Scalars then = scalars(next, m + step);
+    if constexpr (AHEAD == 2) advance(next, m + 2 * step, a.M);
     f2 G[NV][4];
     if (a.w_pre) {
       const float rh = now.rh;
       const f2 rh2 = both(rh);
       f2 ss = both(0.f);
-      wait_copies<2>();  // dn and h'
+      wait_copies<2 + MORE>();  // dn and h'
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         f2 h[4], v[4];
@@ -172,7 +186,7 @@ __global__ void __launch_bounds__(T, 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) G[j][k] = both(0.f);
     }
-    wait_copies<3>();  // dh'
+    wait_copies<3 + MORE>();  // dh'
     const f2 res = both(a.res_scale);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -188,7 +202,7 @@ __global__ void __launch_bounds__(T, 1)
     }
     start_dh(next);
     if (a.dy) {
-      wait_copies<3>();  // y and the gate
+      wait_copies<3 + MORE>();  // y and the gate
       f2 ss = both(0.f);
       const float ry = now.ry, token = now.token;
       const f2 ryk = both(ry * token), bry = both(a.branch_scale * ry);
@@ -261,18 +275,21 @@ __global__ void __launch_bounds__(T, 1)
       }
     }
     start_y(next);
-    if constexpr (ALIGNED) {
-      // A last round without a row: the zero factors would make NaN of an infinity left here.
-      if (r.row && !next.row) {
-        wait_copies<0>();
-        clear_slots<NV, T>(ring, l, next);
-      }
-    }
-    if constexpr (DW && !ALIGNED) group_sync();  // the next row's sums follow this one's
+    if constexpr (AHEAD == 2) advance(next, m + step, a.M);  // again: it was the row after it
+    const bool end = r.row && !next.row;
     r = next;
     now = then;
     m += step;
     parity ^= 1;
+    other();
+    if constexpr (ALIGNED) {
+      // A last round without a row: the zero factors would make NaN of an infinity left here.
+      if (end) {
+        wait_copies<0>();
+        clear_slots<NV, T>(ring, l, r);
+      }
+    }
+    if constexpr (DW && !ALIGNED) group_sync();  // the next row's sums follow this one's
   }
 
   if constexpr (DW && !ALIGNED) {
@@ -399,9 +416,22 @@ cudaError_t launch_bwd(const ResidualNormBwd& a, RowShape s, cudaStream_t st) {
     const int sums = s.rpc * 2 * a.part_ld * static_cast<int>(sizeof(float));
     if (sums > smem) smem = sums;
   }
-  return ws ? launch_rows(residual_norm_bwd_kernel<R, T, PAIR, ALIGNED, DW, true, GF>, s, a, ring,
+  // Two rows ahead where y is not read and a group has more than 6: 4096 x 8192 (without sums of
+  // columns) 59.3 -> 53.4 us, 2048 x 4096 17.2 -> 16.5; with fewer the copies before the first row
+  // cost more than they save (600 x 4096 8.8 -> 9.7), and with y the two sums of a row bound the
+  // loop, not its loads (4096 x 8192 73.5 -> 75.1).
+  if constexpr (ALIGNED && !PAIR && T == 512 && !GF) {
+    const int more = T * ring.slots * 16;
+    const bool reads_y = a.dy && (a.w_post || a.dgate);
+    if (ws && !reads_y && a.M > 6 * s.walkers * s.rpc && smem + more <= kSmemPerCta) {
+      ring.weights += more;
+      return launch_rows(residual_norm_bwd_kernel<R, T, PAIR, ALIGNED, DW, true, GF, 2>, s, a, ring,
+                         smem + more, st);
+    }
+  }
+  return ws ? launch_rows(residual_norm_bwd_kernel<R, T, PAIR, ALIGNED, DW, true, GF, 1>, s, a, ring,
                           smem, st)
-            : launch_rows(residual_norm_bwd_kernel<R, T, PAIR, ALIGNED, DW, false, GF>, s, a, ring,
+            : launch_rows(residual_norm_bwd_kernel<R, T, PAIR, ALIGNED, DW, false, GF, 1>, s, a, ring,
                           smem, st);
 }
 template <typename R, int T, bool PAIR, bool ALIGNED, bool DW>

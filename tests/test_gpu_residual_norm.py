@@ -115,6 +115,18 @@ def test_token_counts(M):
         _check(M, D, seed=M)
 
 
+@pytest.mark.parametrize("M,D,R", [(901, 8192, BF16), (1900, 4096, BF16), (3601, 2040, F32)])
+def test_more_rows_than_are_on_their_way(M, D, R):
+    i, (h, _, r, _), got = _check(M, D, R=R, post=False, gate="none", seed=M)
+    args = dict(rstd_pre=r, w_pre=i["w_pre"], res_scale=0.5, branch_scale=1.25, weight_offset=1.0)
+    frozen = block.residual_norm_backward(i["dn"], i["dh"], h, need_dw=False, branch=True, **args)
+    assert torch.equal(frozen[0], got["dh"]) and torch.equal(frozen[1], got["dy"])
+    # Only as many rows as the others see of theirs: bits do not depend on the batch.
+    few = block.residual_norm_backward(i["dn"][:9], i["dh"][:9], h[:9], need_dw=False, branch=True,
+                                       **{**args, "rstd_pre": r[:9]})
+    assert torch.equal(few[0], got["dh"][:9]) and torch.equal(few[1], got["dy"][:9])
+
+
 @pytest.mark.parametrize("post,gate,pre", list(itertools.product(
     (True, False), ("none", "channel", "token", "full"), (True, False))))
 @pytest.mark.parametrize("R,W,G", [(BF16, BF16, F32), (F32, BF16, BF16), (BF16, F32, BF16),
