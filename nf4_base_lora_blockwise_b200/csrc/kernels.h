@@ -461,6 +461,7 @@ struct AdamTable {
 };
 struct AdamArgs {
   int tensors;
+  int round_bits;        // log2 of a warp's blocks in a chunk (set by launch_adam_step)
   uint32_t blocks;       // of this launch
   int64_t first_block;   // of this launch within the list
   void* m;               // fp32 or 8-bit codes, 256 a block over the list
@@ -483,7 +484,8 @@ struct AdamState {       // device, zero (or the steps taken so far) before the 
   int32_t unused;
   int32_t skipped;       // steps left out for a norm that was not finite
   uint32_t ticket;       // zero between launches
-  int32_t pad[10];
+  uint32_t next;         // chunks drawn; zero between launches
+  int32_t pad[9];
 };
 constexpr int kAdamNormCtas = 148 * 8;  // at most: one double of workspace each
 int adam_norm_ctas(uint32_t blocks);

@@ -146,6 +146,29 @@ def test_more_tensors_than_one_launch(bits):
     _run(sizes, bits=bits, steps=2, max_norm=0.5)
 
 
+@pytest.mark.parametrize("bits,clip", [(8, None), (32, None), (8, 1e9)])
+def test_one_large_tensor_and_its_slices(bits, clip):
+    """The numbering of elements is all that a step depends on: one tensor whose chunks are drawn, and
+    the same memory as 4096 tensors in launches that draw none, leave the same bits."""
+    n, part = 4096 * 2048 - 77, 2048
+    g = torch.Generator().manual_seed(5)
+    p0 = torch.randn(n, generator=g).to(BF16).cuda()
+    grads = [(torch.randn(n, generator=g) * 1e-2).cuda() for _ in range(3)]
+    left = []
+    for split in (False, True):
+        p, grad = p0.clone(), torch.zeros(n, device="cuda")
+        cut = (lambda t: list(t.split(part))) if split else (lambda t: [t])
+        opt = optim.AdamW(cut(p), cut(grad), bits=bits, lr=1e-2, max_grad_norm=clip, seed=3)
+        for d in grads:
+            grad.copy_(d)
+            opt.step()
+        assert opt.steps == 3 and opt.skipped == 0
+        assert int(opt._state[5]) == int(opt._state[6]) == 0        # tickets and chunks drawn
+        left.append([p, opt.m, opt.v] + ([opt.m_scale, opt.v_scale] if bits == 8 else []))
+    for a, b in zip(*left):
+        assert torch.equal(a, b)
+
+
 def test_nothing_beyond_the_workspace_and_state():
     """Guards around the workspace and the state of a list that fills the card stay as they are."""
     n = 40_000_000
