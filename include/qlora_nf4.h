@@ -302,7 +302,8 @@ QLORA_API qlora_status qlora_rope_phase(int rotary_dim, double base, int kind, d
 
 /* One tensor of heads: element i of head h of token (b, s) lies at b batch + s token + h head + i,
  * in elements.  out may be x with the same strides (in place: elements from rotary_dim on are then
- * not touched); otherwise the two must not overlap, and every head is written whole. */
+ * not touched); otherwise the two must not overlap, and every head is written whole.  What is written
+ * for q and for k must not overlap either. */
 typedef struct {
   const void* x;
   void* out;

@@ -45,7 +45,8 @@ def residual_norm_forward(h, y=None, w_pre=None, w_post=None, gate=None, eps=1e-
     with rms(x) = x / sqrt(mean(x^2) + eps).  h [M, D] bf16 or fp32, y [M, D] bf16, weights [D]
     bf16 or fp32, gate None, [D], [M, 1] or [M, D] bf16 or fp32.  Without y only the norm of h is
     taken (h_out is h); without w_pre only the update.  h_out may be h: the stream is then updated
-    in place.  Returns (h_out, n or None, rstd_pre or None, rstd_post or None); the fp32 [M] rstd
+    in place; n may be y.  Other given outputs share no memory with the inputs or each other
+    (ValueError).  Returns (h_out, n or None, rstd_pre or None, rstd_post or None); the fp32 [M] rstd
     are what residual_norm_backward needs (save_rstd=False: not kept)."""
     return (_BIND or _bind()).residual_norm_forward(
         h, y, w_pre, w_post, gate, eps, res_scale, branch_scale, weight_offset, h_out, n, rstd_pre,
@@ -63,7 +64,8 @@ def residual_norm_backward(dn, dh_out, h_out, y=None, rstd_pre=None, rstd_post=N
     gate or w_post was given).
     Returns (dh [M, D] in the residual's type, dy [M, D] bf16 or None, dw_pre and dw_post fp32 [D]
     or None, dgate or None: fp32 [D], fp32 [M, 1], or [M, D] in the gate's type).  dh may be
-    dh_out; frozen norm weights take need_dw=False."""
+    dh_out, dy may be y or dn, else given outputs share no memory with the inputs or each other
+    (ValueError); frozen norm weights take need_dw=False."""
     return (_BIND or _bind()).residual_norm_backward(
         dn, dh_out, h_out, y, rstd_pre, rstd_post, w_pre, w_post, gate, res_scale, branch_scale,
         weight_offset, need_dw, need_dgate, branch, dh, dy, dw_pre, dw_post, dgate, ws)
@@ -133,7 +135,8 @@ def rope(x, positions, plan, n_heads=None, k=None, n_heads_k=None, inverse=False
     [B, S, n, head_dim] views of any strides but 1 in the head.  positions: int32 or int64 tensor,
     one a token, or an int: the first token's, counting up along S (M).  inverse: the backward
     pass, on the gradients.  inplace=False (or out / out_k): to a contiguous tensor of the turned
-    heads, [M, n_heads * head_dim] or x's shape with n_heads.
+    heads, [M, n_heads * head_dim] or x's shape with n_heads.  What is written shares no element
+    with another argument (ValueError): x and k may be parts of one packed row, not overlap.
     Returns the turned x, or (x, k)."""
     return (_BIND or _bind()).rope(
         x, positions, plan.phase, plan.scale, plan.head_dim, plan.rotary_dim, plan.interleaved,

@@ -15,10 +15,15 @@
 // rows in groups of tpr threads with a barrier of their own.  A thread copies what it reads
 // itself into its own slots by cp.async and starts the next row's copy as soon as it has read a
 // slot for the last time, so a row is on its way while the one before is worked on, without a
-// barrier or a second stage.
+// barrier or a second stage.  (Slots laid out by thread instead of by granule: 36 us against 26 at
+// 4096 x 4096; scalar fp32 instead of pairs: 27.5 against 26.2.)
+// Measured, bf16 with both norms and a channel gate: 4096 x 4096 24 us, 5.6 TB/s; without the gate
+// 16384 x 8192 164 us, 6.5 TB/s.  1 x 4096: 2.3 us.
 //
 // Rows of D % 8 != 0 start anywhere in a 16-byte granule: threads copy and store the granules as
-// they lie, and address what belongs to columns by the row's offset (residual_norm.cuh).
+// they lie, and address what belongs to columns by the row's offset (residual_norm.cuh).  1531 x 2051
+// with an fp32 residual and a whole gate: 15.8 us, 2.8 TB/s, bound by the instructions of that
+// (rows joined from two granules by shuffles: 20.7 us).
 #include "residual_norm.cuh"
 
 namespace qlora {

@@ -33,7 +33,9 @@ class AdamW:
     rounding, which is reproducible.  step: steps taken before.
 
     State: m, v: flat over the list, tensor i from offsets[i] on (every tensor starts a block of
-    256 elements): fp32, or uint8 codes with the blocks' fp32 m_scale, v_scale.
+    256 elements): fp32, or uint8 codes with the blocks' fp32 m_scale, v_scale.  It is zeroed on the
+    stream current at construction; the caller orders steps on other streams after that, and
+    one step after another.
     """
 
     def __init__(self, params, grads, masters=None, bits=32, lr=1e-4, betas=(0.9, 0.999), eps=1e-8,

@@ -6,7 +6,11 @@ step fixes another precision) of what the GPU library computes:
 * ``oracle.nf4``   -- the 4-bit NormalFloat codebook, blockwise absmax quantisation, nibble
   packing, the double-quantised absmax variant and dequantisation;
 * ``oracle.qlora`` -- the LoRA-adapted linear forward ``h = X deq(W0)^T + (alpha/r) (X A^T) B^T``
-  and its hand-derived backward, plus the SwiGLU glue used by the MLP workload.
+  and its hand-derived backward, plus the SwiGLU glue used by the MLP workload;
+* ``oracle.lm_head`` -- the LM head with its cross-entropy;
+* ``oracle.block`` -- the residual update with its norms, and rotary positions, with their
+  backward;
+* ``oracle.optim`` -- AdamW, and the 8-bit codes of its moments.
 
 Rules this package keeps:
 
