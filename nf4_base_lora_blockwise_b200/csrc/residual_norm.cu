@@ -22,7 +22,7 @@
 //
 // Rows of D % 8 != 0 start anywhere in a 16-byte granule: threads copy and store the granules as
 // they lie, and address what belongs to columns by the row's offset (residual_norm.cuh).  1531 x 2051
-// with an fp32 residual and a whole gate: 15.8 us, 2.8 TB/s, bound by the instructions of that
+// with an fp32 residual and a whole gate: 14.9 us, 3.0 TB/s, bound by the instructions of that
 // (rows joined from two granules by shuffles: 20.7 us).
 #include "residual_norm.cuh"
 

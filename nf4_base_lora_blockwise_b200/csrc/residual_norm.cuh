@@ -353,10 +353,24 @@ __device__ __forceinline__ void stage_weights(const Weights& w, const Ring& ring
       }
     }
   } else {
-    for (int c = tid - 8; c < ring.width + 16; c += threads) {
-      const bool in = first + c >= 0 && first + c < w.D;
-      if (w.w_pre) d[skewed(c)] = in ? combine1<0>(w, first + c) : 0.f;
-      if (second) d[ring.weights_ld + skewed(c)] = in ? combine1<1>(w, first + c) : 0.f;
+    // Four columns' loads at a time: a CTA of few rows has few threads, which would wait for each.
+    constexpr int U = 4;
+    for (int c0 = tid - 8; c0 < ring.width + 16; c0 += threads * U) {
+      float f[U], g[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int c = c0 + u * threads;
+        const bool in = first + c >= 0 && first + c < w.D;
+        f[u] = in && w.w_pre ? combine1<0>(w, first + c) : 0.f;
+        g[u] = in && second ? combine1<1>(w, first + c) : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int c = c0 + u * threads;
+        if (c >= ring.width + 16) break;
+        if (w.w_pre) d[skewed(c)] = f[u];
+        if (second) d[ring.weights_ld + skewed(c)] = g[u];
+      }
     }
   }
 }
