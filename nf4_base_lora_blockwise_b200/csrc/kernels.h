@@ -438,7 +438,8 @@ struct RopeArgs {
   bool f32, pos64, interleaved, inverse, copy;  // copy: out of place, the rest of each head too
   float scale;
 };
-cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream);
+// *launches: kernels launched.
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream, int* launches);
 
 // ------------------------------ AdamW over many tensors -------------------------------------
 // Blocks of 256 elements are numbered through the list of tensors, each tensor starting one.

@@ -1532,8 +1532,9 @@ qlora_status qlora_rope(const qlora_rope_heads* q, const qlora_rope_heads* k, in
   a.inverse = inverse != 0;
   a.copy = !in_place;
   a.scale = scale;
-  st = cuda_status(launch_rope(a, static_cast<cudaStream_t>(stream)));
-  if (st == QLORA_OK) count(1);
+  int n = 0;
+  st = cuda_status(launch_rope(a, static_cast<cudaStream_t>(stream), &n));
+  if (st == QLORA_OK) count(n);
   return st;
 }
 

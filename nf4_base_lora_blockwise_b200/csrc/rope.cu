@@ -18,6 +18,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "divide.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
 #include "vec.cuh"
@@ -33,17 +34,6 @@ constexpr int kRopeTokens = 8;     // tokens of a CTA at most
 // 10 % slower: fewer CTAs fit.)
 constexpr int kRopePairs = 2, kRopeSingles = 4;
 constexpr int kRopeCtas = 4 * 148;  // that the SMs hold at a time
-
-// n / d for n d < 2^32, by one high product.
-struct Divide {
-  uint32_t mul, d;
-};
-Divide divide_by(uint32_t d) {
-  return {static_cast<uint32_t>((0x100000000ull + d - 1) / d), d};  // (0 for d = 1: see below)
-}
-__device__ __forceinline__ uint32_t quotient(uint32_t n, Divide v) {
-  return v.d == 1 ? n : __umulhi(n, v.mul);
-}
 
 // Work of one token: items of VEC elements (interleaved) or VEC pairs (halves), `groups` a head and
 // the heads of both tensors one after the other; then `copies` a head of VEC elements that pass.
@@ -235,14 +225,19 @@ int rope_vec(const RopeArgs& a) {
   return 1;
 }
 
-}  // namespace
+// Items of a head that are turned, and copied ones, in vectors of vec.
+int turned_items(const RopeArgs& a, int vec) {
+  return a.interleaved ? a.rotary_dim / (vec < 2 ? 2 : vec) : a.rotary_dim / 2 / vec;
+}
+int copied_items(const RopeArgs& a, int vec) {
+  return a.copy ? (a.head_dim - a.rotary_dim) / vec : 0;
+}
 
-cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream) {
-  const int vec = rope_vec(a);
+// One launch, of no more heads than its divisions are exact for.
+cudaError_t launch_heads(const RopeArgs& a, int vec, cudaStream_t stream) {
   const int half = a.rotary_dim / 2;
   const int heads = a.t[0].heads + a.t[1].heads;
-  const int groups = a.interleaved ? a.rotary_dim / (vec < 2 ? 2 : vec) : half / vec;
-  const int copies = a.copy ? (a.head_dim - a.rotary_dim) / vec : 0;
+  const int groups = turned_items(a, vec), copies = copied_items(a, vec);
   RopeShape s;
   s.turned = heads * groups;
   s.items = heads * (groups + copies);
@@ -287,6 +282,33 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream) {
   if (vec == 4) return launch<__nv_bfloat16, 4>(a, s, grid, stream);
   if (vec == 2) return launch<__nv_bfloat16, 2>(a, s, grid, stream);
   return launch<__nv_bfloat16, 1>(a, s, grid, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t stream, int* launches) {
+  const int vec = rope_vec(a);
+  const int copied = exact_heads(copied_items(a, vec)), turned = exact_heads(turned_items(a, vec));
+  const int most = copied < turned ? copied : turned;
+  if (a.t[0].heads + a.t[1].heads <= most) {
+    *launches = 1;
+    return launch_heads(a, vec, stream);
+  }
+  // Out of place, over 1000 heads that copy over 1000 elements each, one by one: some heads a launch.
+  for (const RopeHeads& h : a.t)
+    for (int first = 0; first < h.heads; first += most) {
+      RopeArgs some = a;
+      RopeHeads& t = some.t[0];
+      t = h;
+      t.heads = h.heads - first < most ? h.heads - first : most;
+      t.x = static_cast<const char*>(h.x) + first * h.x_head * (a.f32 ? 4 : 2);
+      t.out = static_cast<char*>(h.out) + first * h.out_head * (a.f32 ? 4 : 2);
+      some.t[1] = RopeHeads{};
+      const cudaError_t e = launch_heads(some, vec, stream);
+      if (e != cudaSuccess) return e;
+      ++*launches;
+    }
+  return cudaSuccess;
 }
 
 }  // namespace qlora

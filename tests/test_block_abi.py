@@ -226,3 +226,35 @@ def test_binding_raises():
             f(None)
     with pytest.raises(TypeError):
         b.current_stream("x")
+
+
+def test_divisions_of_rope_are_exact(tmp_path):
+    """csrc/divide.cuh, compiled for the host: for every number of items that a head can have, below
+    and at every multiple, as far as the 4096 heads of a call reach or the heads of one launch do.
+    Past these the quotient is wrong for some divisor (2046: from head 1028 on)."""
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("g++ not available")
+    src = tmp_path / "divide.cpp"
+    src.write_text('#include "divide.cuh"\n#include <cstdio>\n'
+                   'int main() {\n'
+                   '  unsigned long long wrong = 0, split = 0;\n'
+                   '  for (uint32_t d = 1; d <= 2048; ++d) {\n'
+                   '    const qlora::Divide v = qlora::divide_by(d);\n'
+                   '    const uint32_t most = qlora::exact_heads(d);\n'
+                   '    const uint32_t heads = most < 4096 ? most : 4096;\n'
+                   '    split += most < 4096;\n'
+                   '    for (uint32_t h = 0; h < heads; ++h)\n'
+                   '      wrong += qlora::quotient(h * d, v) != h || qlora::quotient(h * d + d - 1, v) != h;\n'
+                   '  }\n'
+                   '  const qlora::Divide v = qlora::divide_by(2046);\n'
+                   '  std::printf("%llu %llu %u %d", wrong, split, qlora::quotient(2105333, v), qlora::exact_heads(0));\n'
+                   '}\n')
+    exe = tmp_path / "divide"
+    inc = os.path.join(ROOT, "nf4_base_lora_blockwise_b200", "csrc")
+    subprocess.run([gxx, "-std=c++17", "-O2", "-Wall", "-Werror", "-I" + inc, str(src), "-o",
+                    str(exe)], check=True)
+    got = [int(x) for x in subprocess.run([str(exe)], capture_output=True, text=True,
+                                          check=True).stdout.split()]
+    # 4096 d^2 > 2^32 for d > 1024.
+    assert got == [0, 2048 - 1024, 2105333 // 2046 + 1, 2 ** 31 - 1]

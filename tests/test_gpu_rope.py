@@ -218,3 +218,18 @@ def test_what_is_written_is_apart():
     for hd, rd in ((0, 0), (64, 0), (32, 64)):
         with pytest.raises(ValueError):
             block.rope(x, 0, block.RopePlan(plan.phase[:rd // 2], 1.0, hd, rd))
+
+
+@pytest.mark.parametrize("heads,heads_k,rd", [(4096, None, 2), (1100, 1029, 2), (2049, 2047, 4),
+                                              (1200, None, 1024), (4096, None, 2048)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_the_most_and_widest_heads(heads, heads_k, rd, interleaved):
+    """Up to 4096 heads of 2048, few of whose elements are turned: every copied element of every head
+    is written once, from its own place."""
+    plan = block.rope_plan(2048, rotary_dim=rd, interleaved=interleaved)
+    x = _rnd(1, heads, 2048, seed=rd)
+    k = None if heads_k is None else _rnd(1, heads_k, 2048, seed=rd + 1)
+    outs = block.rope(x, 777, plan, k=k, out=torch.zeros_like(x),
+                      out_k=None if k is None else torch.zeros_like(k))
+    for got, of in zip([outs] if k is None else outs, (x, k)):
+        _agree(got, of, [777], plan, 10000.0, None, False)
