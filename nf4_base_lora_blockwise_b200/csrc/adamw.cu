@@ -23,7 +23,7 @@
 // grid's least value are rare and made by a second pass over the warp's block.
 // Measured: 42 M fp32 elements and moments, no norm (28 bytes an element) 233 us, 6.5 TB/s; 42 M bf16
 // ones in 448 tensors with masters, 8-bit moments and the clip, and the moments read as bf16 after
-// it, 217 us; 1.3 M in 14 tensors, 32 bits and the clip, 12.5 us.
+// it, 220 us; 1.3 M in 14 tensors, 32 bits and the clip, 13.9 us.
 #include <cuda_bf16.h>
 
 #include <cstdint>
@@ -260,11 +260,6 @@ __global__ void __launch_bounds__(kAdamThreads, 3)
   __shared__ int ahead_ti[2];
   __shared__ CodeTables codes;
   if constexpr (BITS8) fill_tables(codes);
-  // A norm kernel in front has waited for what precedes it before it let this one start, and
-  // writes no tensor: only its sums have to be waited for, after the first loads and the
-  // corrections.
-  if (!a.use_norm) pdl_wait();
-  AdamState* st = static_cast<AdamState*>(a.state);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // The CTA's chunks of blocks: two by its place, the others by tickets.  The chunk after the
   // current one is known, so that its first blocks can be on their way.
@@ -275,23 +270,28 @@ __global__ void __launch_bounds__(kAdamThreads, 3)
   uint32_t chunk = blockIdx.x, drawn = 0;
   uint32_t b = (chunk << size_bits) + warp;
   int round = 0, parity = 0, ti = 0;
-  Held<BITS8> h;
-  if (b < a.blocks) {  // the first block is on its way while the corrections are worked out
-    ti = tensor_of(table, a.tensors, b);
-    load_block(table.t[ti], a, b, lane, h);
-  }
+  if (b < a.blocks) ti = tensor_of(table, a.tensors, b);
   if (threadIdx.x == 0) {
-    step_s = st->step + 1;
-    corrections(a, step_s, &sc[0], &sc[1]);
     ahead[0] = chunk + gridDim.x;
     ahead_ti[0] = ahead[0] < chunks ? tensor_of(table, a.tensors, ahead[0] << size_bits) : 0;
     ahead[1] = chunks;
   }
+  // What earlier kernels wrote is promised after this grid's own wait only, so nothing is read before
+  // it, though the norm's kernel in front has waited for them.  (With the first loads ahead of it: one
+  // block's adapters 12.5 us instead of 13.9, the 8B ones in 8 bits 217 instead of 220.)
+  pdl_wait();
+  AdamState* st = static_cast<AdamState*>(a.state);
+  Held<BITS8> h;
+  if (b < a.blocks)  // the first block is on its way while the corrections are worked out
+    load_block(table.t[ti], a, b, lane, h);
+  if (threadIdx.x == 0) {
+    step_s = st->step + 1;
+    corrections(a, step_s, &sc[0], &sc[1]);
+  }
   float factor = static_cast<float>(a.grad_scale);
   if (a.use_norm) {
-    pdl_wait();
     double t = 0.0;
-    for (int i = threadIdx.x; i < a.part_count; i += kAdamThreads) t += __ldcg(a.part + i);
+    for (int i = threadIdx.x; i < a.part_count; i += kAdamThreads) t += a.part[i];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
     if (lane == 0) parts[warp] = t;
