@@ -547,8 +547,9 @@ template <typename K, typename A>
 cudaError_t launch_rows(K kernel, const RowShape& s, const A& a, const Ring& ring, int smem,
                         cudaStream_t stream) {
   if (smem > 40 * 1024) {
+    // Always the same: a call of another host thread must not lower what this launch takes.
     const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerCta);
     if (e != cudaSuccess) return e;
   }
   const int cluster = s.pair ? 2 : 1;

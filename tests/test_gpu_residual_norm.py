@@ -10,13 +10,17 @@ tokens add at most M sequential additions: C = 256 + M.  n is checked against th
 library stored it, which is its definition.
 """
 
+import ctypes
 import itertools
+import os
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
 import torch
 
-from nf4_base_lora_blockwise_b200 import block
+from nf4_base_lora_blockwise_b200 import abi, block
 from oracle import block as oracle
 
 pytestmark = pytest.mark.gpu
@@ -327,3 +331,59 @@ def test_given_outputs_are_apart():
                dict(dw_pre=col, dw_post=col), dict(dw_pre=col, dgate=col)):
         with pytest.raises(ValueError, match="shares memory"):
             g(**kw)
+
+
+CALLER = r"""
+#include <pthread.h>
+#include <stdint.h>
+#include "qlora_nf4.h"
+typedef qlora_status (*call_t)(const void*, const void*, const void*, const void*, const void*, int,
+                               int64_t, int, int, float, float, float, float, void*, void*, float*,
+                               float*, qlora_stream_t);
+typedef struct { call_t call; const void *h, *w; void* n; int D, calls; qlora_stream_t s; int status; } job;
+static void* work(void* p) {
+  job* j = (job*)p;
+  for (int i = 0; i < j->calls && j->status == QLORA_OK; ++i)
+    j->status = j->call(j->h, 0, j->w, 0, 0, 0, 1, j->D, 0, 1e-5f, 1.f, 1.f, 0.f, 0, j->n, 0, 0, j->s);
+  return 0;
+}
+int two(job* a, job* b) {
+  pthread_t t;
+  if (pthread_create(&t, 0, work, a)) return -1;
+  work(b);
+  return pthread_join(t, 0);
+}
+"""
+
+
+def test_host_threads_at_once(tmp_path):
+    """Calls of one kernel that take little and much shared memory, from two host threads on two
+    streams: neither changes what the other's launch may take."""
+    gcc = shutil.which("gcc")
+    if gcc is None:
+        pytest.skip("gcc not available")
+    (tmp_path / "caller.c").write_text(CALLER)
+    lib = tmp_path / "caller.so"
+    include = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include")
+    subprocess.run([gcc, "-shared", "-fPIC", "-O1", "-pthread", "-I" + include,
+                    str(tmp_path / "caller.c"), "-o", str(lib)], check=True)
+
+    class Job(ctypes.Structure):
+        _fields_ = [("call", ctypes.c_void_p), ("h", ctypes.c_void_p), ("w", ctypes.c_void_p),
+                    ("n", ctypes.c_void_p), ("D", ctypes.c_int), ("calls", ctypes.c_int),
+                    ("s", ctypes.c_void_p), ("status", ctypes.c_int)]
+
+    call = ctypes.cast(abi._lib().qlora_residual_norm_fwd, ctypes.c_void_p).value
+    keep, jobs = [], []
+    for D in (33, 16375):
+        s = torch.cuda.Stream()
+        h, w = (torch.ones(*shape, dtype=BF16, device="cuda") for shape in ((1, D), (D,)))
+        n = torch.empty_like(h)
+        keep.append((s, h, w, n))
+        jobs.append(Job(call, h.data_ptr(), w.data_ptr(), n.data_ptr(), D, 20000, s.cuda_stream, 0))
+    torch.cuda.synchronize()
+    assert ctypes.CDLL(str(lib)).two(ctypes.byref(jobs[0]), ctypes.byref(jobs[1])) == 0
+    torch.cuda.synchronize()
+    assert [j.status for j in jobs] == [0, 0]
+    for _, h, _, n in keep:
+        assert torch.allclose(n.float(), h.float(), rtol=2.0 ** -8)
