@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kAdamThreads, 3)
       const int64_t gb = a.first_block + b;           // block of the list
       const int64_t e0 = gb * kAdamBlock + lane * 8;  // element of the list
       const float rate = lr * t.lr_scale;
-      const f2 keep = both(1.f - rate * t.weight_decay), move = both(-rate * c1);
+      const f2 decay = both(-rate * t.weight_decay), move = both(-rate * c1);
       f2 m2[4], v2[4];
       float vmax = 0.f, vmin = 0.f;
 #pragma unroll
@@ -365,7 +365,9 @@ __global__ void __launch_bounds__(kAdamThreads, 3)
       for (int k = 0; k < 4; ++k) {
         const float2 d = split(fma2(root[k], c2, eps)), mm = split(m2[k]);
         const f2 u = pair(__fdividef(mm.x, d.x), __fdividef(mm.y, d.y));
-        const float2 q = split(fma2(u, move, mul2(pair(h.p[2 * k], h.p[2 * k + 1]), keep)));
+        // (p + (decay + move), not p (1 - lr wd) + move: 1 - lr wd would round lr wd to 2^-24.)
+        const f2 ph = pair(h.p[2 * k], h.p[2 * k + 1]);
+        const float2 q = split(add2(ph, fma2(u, move, mul2(ph, decay))));
         p[2 * k] = q.x;
         p[2 * k + 1] = q.y;
       }

@@ -376,3 +376,23 @@ def test_refusals():
     q.data, g.data = z(1), z(1)
     opt.step()
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("lr,wd", [(2e-6, 0.01), (5e-6, 0.01), (2e-5, 0.01), (4e-4, 0.01),
+                                   (1e-3, 0.1)])
+@pytest.mark.parametrize("param", ["f32", "master"])
+def test_small_decays_are_rounded_once(lr, wd, param):
+    """p - lr wd p is rounded with p, not as 1 - lr wd before: for p in [1, 2) off by half a step, 2^-24,
+    and by the roundings of lr, wd, their product and its product with p, 2^-22 of the decay."""
+    n = 1 << 20
+    p = 1.0 + torch.arange(n, dtype=torch.float64, device="cuda").div(n).float()
+    before = p.double()
+    grad = torch.zeros(n, device="cuda")
+    if param == "f32":
+        opt = optim.AdamW([p], [grad], lr=lr, weight_decay=wd)
+    else:
+        opt = optim.AdamW([p.to(BF16)], [grad], [p], bits=8, lr=lr, weight_decay=wd)
+    opt.step()
+    decay = lr * wd * before
+    err = (p.double() - (before - decay)).abs()
+    assert torch.all(err <= U + 4 * U * decay), float((err / (U + 4 * U * decay)).max())
