@@ -329,8 +329,9 @@ QLORA_API qlora_status qlora_rope(const qlora_rope_heads* q, const qlora_rope_he
  *   p = p (1 - lr wd) - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps),  t: this step, from 1
  * with lr the tensor's lr x lr_scale and wd its weight_decay.  max_norm > 0:
  * clip = min(1, max_norm / (norm + 1e-6)), norm = ||grad_scale grad|| over all tensors; with
- * max_norm > 0 or check_finite the norm is computed first, and where it is not finite the call
- * changes nothing but the state's norm and its count of skipped steps.
+ * max_norm > 0 or check_finite the norm is computed first (in 64 bits, so that squares do not
+ * overflow), and where it is not finite as the float that the state holds the call changes nothing
+ * but the state's norm and its count of skipped steps.
  *   p       bf16, or fp32 with param_f32; read and written.  master: an fp32 copy that the step is
  *           taken on (p is its bf16 rounding), or NULL: a bf16 p is then rounded stochastically.
  *   grad    bf16, or fp32 with grad_f32.

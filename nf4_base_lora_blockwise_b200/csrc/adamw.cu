@@ -2,7 +2,7 @@
 //   g = grad_scale clip grad,  m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g^2
 //   p = p (1 - lr wd) - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
 //   clip = min(1, max_norm / (||grad_scale grad|| + 1e-6)) over all tensors; a norm that is not
-//   finite leaves parameters, moments and the step count as they are.
+//   finite as an fp32 number leaves parameters, moments and the step count as they are.
 //
 // 8-bit moments, in blocks of 256 elements with one fp32 scale, the block's largest magnitude:
 //   m: a sign and a float of 4 exponent and 3 mantissa bits of |m| / scale;
@@ -305,9 +305,10 @@ __global__ void __launch_bounds__(kAdamThreads, 3)
     const double norm = sqrt(t) * fabs(a.grad_scale);
     if (a.max_norm > 0.0)
       factor = static_cast<float>(a.grad_scale * fmin(1.0, a.max_norm / (norm + 1e-6)));
-    const bool ok = isfinite(norm);
+    const float reported = static_cast<float>(norm);
+    const bool ok = isfinite(reported);  // what the caller sees decides
     if (a.last && blockIdx.x == 0 && threadIdx.x == 0) {
-      st->norm = static_cast<float>(norm);
+      st->norm = reported;
       st->skipped += !ok;
     }
     if (!ok) return;  // the whole step is left out

@@ -29,7 +29,8 @@ class AdamW:
     at every step.  lr_scales, weight_decays: one value a tensor (default 1 and weight_decay).
     max_grad_norm: clips the norm over all gradients (None: not); grad_scale multiplies them first.
     check_finite: computes the norm without a clip too.  Where the norm is computed and is not
-    finite the step changes nothing but ``grad_norm`` and ``skipped``.  seed: of the stochastic
+    finite (as the fp32 number that step() returns) the step changes nothing but that and
+    ``skipped``.  seed: of the stochastic
     rounding, which is reproducible.  step: steps taken before.
 
     State: m, v: flat over the list, tensor i from offsets[i] on (every tensor starts a block of

@@ -396,3 +396,20 @@ def test_small_decays_are_rounded_once(lr, wd, param):
     decay = lr * wd * before
     err = (p.double() - (before - decay)).abs()
     assert torch.all(err <= U + 4 * U * decay), float((err / (U + 4 * U * decay)).max())
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("scale,applied", [(1.0, False), (1e-4, True)])
+def test_the_reported_norm_decides(bits, scale, applied):
+    """A norm past fp32's largest number, though the 64-bit sum holds it, is an infinity: what step()
+    returns says whether the step was taken."""
+    params, grads, masters = _lists([600, 300], "master", F32, 4)
+    for g in grads:
+        g.fill_(3e38)
+    opt = optim.AdamW(params, grads, masters, bits=bits, max_grad_norm=1.0, grad_scale=scale)
+    before = [t.clone() for t in (*params, *masters, opt.m, opt.v)]
+    norm = opt.step()
+    assert torch.isfinite(norm).item() == applied
+    assert (opt.steps, opt.skipped) == ((1, 0) if applied else (0, 1))
+    same = [torch.equal(a, b) for a, b in zip(before, (*params, *masters, opt.m, opt.v))]
+    assert not any(same[2:4]) if applied else all(same)
