@@ -265,7 +265,8 @@ __global__ void __launch_bounds__(T, 1)
           static_cast<float*>(a.dgate)[m] = a.branch_scale * ry * s;
       }
       const float brk = a.branch_scale * token;
-      const f2 ct = both(post ? brk * ry : brk), cy = both(-brk * ry * ry * ry * s * inv_d);
+      // (The sum holds y once: its product with r_y first, a cube of r_y leaves fp32 sooner.)
+      const f2 ct = both(post ? brk * ry : brk), cy = both(-(brk * ry) * (ry * s * inv_d * ry));
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
 #pragma unroll

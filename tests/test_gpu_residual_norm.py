@@ -387,3 +387,14 @@ def test_host_threads_at_once(tmp_path):
     assert [j.status for j in jobs] == [0, 0]
     for _, h, _, n in keep:
         assert torch.allclose(n.float(), h.float(), rtol=2.0 ** -8)
+
+
+@pytest.mark.parametrize("size", [2.0 ** -44, 2.0 ** 50])
+@pytest.mark.parametrize("D", [264, 37, 8200])
+def test_branches_of_any_size(size, D):
+    """The branch's norm takes any size out of y: cubes of its 1 / rms, past both ends of fp32 here,
+    do not enter the gradients."""
+    def change(i):
+        i["y"] *= size
+    _check(6, D, change=change, eps=0.0, seed=D)
+    _check(6, D, R=F32, W=F32, gate="token", change=change, eps=0.0, seed=D)
