@@ -235,7 +235,8 @@ QLORA_API qlora_status qlora_swiglu_packed_bwd(const void* gu, const void* da, v
  * and w_post fp32 with QLORA_F32_WEIGHTS; the gate fp32 with QLORA_F32_GATE.  The gate is NULL,
  * [D], [M] or [M, D] by gate_kind.  rstd_pre, rstd_post [M] fp32 are kept for the backward (NULL:
  * not kept).  fp32 arithmetic, one rounding at each output.  1 <= D <= 16384, and <= 16376 where
- * D % 8 != 0; M >= 0 (M = 0 does nothing).  h_out may be h, n may be y. */
+ * D % 8 != 0; M >= 0 (M = 0 does nothing); eps >= 0, the scales and the offset finite.  h_out may be
+ * h, n may be y. */
 enum { QLORA_F32_RESIDUAL = 1, QLORA_F32_WEIGHTS = 2, QLORA_F32_GATE = 4 };
 enum { QLORA_GATE_NONE = 0, QLORA_GATE_CHANNEL = 1, QLORA_GATE_TOKEN = 2, QLORA_GATE_FULL = 3 };
 QLORA_API qlora_status qlora_residual_norm_fwd(const void* h, const void* y, const void* w_pre,

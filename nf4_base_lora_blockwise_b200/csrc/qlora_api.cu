@@ -1320,6 +1320,9 @@ qlora_status qlora_residual_norm_fwd(const void* h, const void* y, const void* w
   if (M < 0 || !norm_width(D) || gate_kind < QLORA_GATE_NONE ||
       gate_kind > QLORA_GATE_FULL || (types & ~7))
     return QLORA_ERR_SHAPE;
+  if (!(eps >= 0.f) || !finite_f(eps) || !finite_f(res_scale) || !finite_f(branch_scale) ||
+      !finite_f(weight_offset))
+    return QLORA_ERR_SHAPE;
   // What nothing would write or read is a mistake of the caller's.
   if (!y && (h_out || w_post || rstd_post || gate_kind != QLORA_GATE_NONE))
     return QLORA_ERR_SHAPE;
@@ -1380,6 +1383,8 @@ qlora_status qlora_residual_norm_bwd(const void* dn, const void* dh_out, const v
   if (M < 0 || !norm_width(D) || gate_kind < QLORA_GATE_NONE ||
       gate_kind > QLORA_GATE_FULL || (types & ~7) ||
       (gate_kind == QLORA_GATE_NONE && (gate || dgate)))
+    return QLORA_ERR_SHAPE;
+  if (!finite_f(res_scale) || !finite_f(branch_scale) || !finite_f(weight_offset))
     return QLORA_ERR_SHAPE;
   for (const void* p :
        {dn, dh_out, h_out, y, static_cast<const void*>(rstd_pre),

@@ -234,8 +234,7 @@ PyObject* residual_norm_forward(PyObject*, PyObject* const* a, Py_ssize_t na) {
     apart({{"h_out", given_h}, {"n", given_n}, {"rstd_pre", given_pre}, {"rstd_post", given_post}},
           {{"h", &h}, {"y", y}, {"w_pre", w.w_pre}, {"w_post", w.w_post}, {"gate", w.gate}},
           {{given_h, &h}, {given_n, y}});
-  if (M > 0 &&
-      failed("qlora_residual_norm_fwd",
+  if (failed("qlora_residual_norm_fwd",
              qlora_residual_norm_fwd(ptr(h), ptr(y), ptr(w.w_pre), ptr(w.w_post), ptr(w.gate),
                                      w.kind, M, static_cast<int>(D), w.types,
                                      static_cast<float>(number(a[5])), static_cast<float>(res),

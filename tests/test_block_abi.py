@@ -258,3 +258,21 @@ def test_divisions_of_rope_are_exact(tmp_path):
                                           check=True).stdout.split()]
     # 4096 d^2 > 2^32 for d > 1024.
     assert got == [0, 2048 - 1024, 2105333 // 2046 + 1, 2 ** 31 - 1]
+
+
+def test_norm_refuses_numbers_out_of_range(lib):
+    """eps is not negative, the scales and the offset are finite (as fp32 numbers)."""
+    fwd = lambda eps, res=1.0, br=1.0, o=0.0, M=4: lib.qlora_residual_norm_fwd(  # noqa: E731
+        FAKE, FAKE, FAKE, None, None, 0, M, 64, 0, eps, res, br, o, FAKE, FAKE, None, None, None)
+    bwd = lambda res, br, o: lib.qlora_residual_norm_bwd(  # noqa: E731
+        FAKE, FAKE, FAKE, None, FAKE, None, FAKE, None, None, 0, 4, 64, 0, res, br, o, FAKE, FAKE,
+        None, None, None, None, 0, None)
+    inf, nan = float("inf"), float("nan")
+    assert fwd(0.0, M=0) == 0
+    for eps in (-1e-5, nan, inf, -inf, 1e39):
+        assert fwd(eps) == fwd(eps, M=0) == SHAPE, eps
+    for x in (nan, inf, -inf):
+        for at in range(3):
+            args = [1.0, 1.0, 0.0]
+            args[at] = x
+            assert fwd(1e-5, *args) == SHAPE and bwd(*args) == SHAPE, args
