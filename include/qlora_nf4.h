@@ -350,6 +350,7 @@ QLORA_API qlora_status qlora_rope(const qlora_rope_heads* q, const qlora_rope_he
  * lr_device: device float that takes the place of lr, or NULL.  ws: device scratch of
  * qlora_adamw_workspace_bytes() bytes, needed with max_norm or check_finite.  A state and its ws
  * belong to one sequence of calls.  n = 0 tensors are allowed; p, grad and master 16-byte aligned.
+ * lr, grad_scale, every lr_scale and weight_decay are finite, 0 <= beta1, beta2 < 1, eps >= 0.
  * Captured into a graph, a replay takes the next step. */
 typedef struct {
   void* p;

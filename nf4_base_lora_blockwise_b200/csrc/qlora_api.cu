@@ -1573,7 +1573,9 @@ qlora_status qlora_adamw_step(const qlora_adamw_tensor* tensors, int count_,
     return QLORA_ERR_SHAPE;
   for (int i = 0; i < count_; ++i) {
     const qlora_adamw_tensor& t = tensors[i];
-    if (t.n < 0 || t.n > (int64_t{1} << 38) || (t.master && t.param_f32)) return QLORA_ERR_SHAPE;
+    if (t.n < 0 || t.n > (int64_t{1} << 38) || (t.master && t.param_f32) ||
+        !finite_f(t.lr_scale) || !finite_f(t.weight_decay))
+      return QLORA_ERR_SHAPE;
     if (t.n == 0) continue;
     if (!t.p || !t.grad) return QLORA_ERR_NULL;
     if (!aligned16(t.p) || !aligned16(t.master) || !aligned16(t.grad)) return QLORA_ERR_ALIGN;

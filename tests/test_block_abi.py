@@ -276,3 +276,11 @@ def test_norm_refuses_numbers_out_of_range(lib):
             args = [1.0, 1.0, 0.0]
             args[at] = x
             assert fwd(1e-5, *args) == SHAPE and bwd(*args) == SHAPE, args
+
+
+def test_adamw_refuses_rates_that_are_not_finite(lib):
+    T = abi.AdamWTensor
+    for x in (float("nan"), float("inf"), -float("inf")):
+        for n in (8, 0):
+            assert _adam(lib, t=T(FAKE, FAKE, FAKE, n, x, 0, 0, 0)) == SHAPE
+            assert _adam(lib, t=T(FAKE, FAKE, FAKE, n, 1, x, 0, 0)) == SHAPE
