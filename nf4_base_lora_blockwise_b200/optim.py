@@ -76,6 +76,11 @@ class AdamW:
                                                g.dtype is torch.float32)
             self.offsets.append(at)
             at += -(-p.numel() // _BLOCK) * _BLOCK
+        self._lr = lr if isinstance(lr, torch.Tensor) else None
+        if self._lr is not None:
+            if self._lr.numel() != 1:
+                raise ValueError("lr: expected one element")
+            self._check(self._lr, (torch.float32,), self._lr.shape, "lr")
         self._no_overlap()
         blocks = at // _BLOCK
         kind = torch.uint8 if bits == 8 else torch.float32
@@ -90,11 +95,6 @@ class AdamW:
         if step:
             self._state.view(torch.int64)[0] = step
         self._norm = self._state.view(torch.float32)[2:3]
-        self._lr = lr if isinstance(lr, torch.Tensor) else None
-        if self._lr is not None:
-            if self._lr.numel() != 1:
-                raise ValueError("lr: expected one element")
-            self._check(self._lr, (torch.float32,), self._lr.shape, "lr")
         self._config = abi.AdamWConfig(0.0 if self._lr is not None else lr, betas[0], betas[1],
                                        eps, grad_scale, max_grad_norm or 0.0, _ptr(self._lr),
                                        seed & 0xFFFFFFFF, bits, bool(check_finite))
@@ -115,19 +115,20 @@ class AdamW:
                              f"(strides {t.stride()}) on {t.device}")
 
     def _no_overlap(self):
-        """Parameters and masters are written: no two of them, nor one and a gradient, may share
-        memory."""
+        """Parameters and masters are written: no two of them, nor one and a gradient or the
+        learning rate, may share memory."""
         spans = []
-        for kind, ts in zip(("params", "masters", "grads"), self._bound):
+        for kind, ts in zip(("params", "masters", "grads", "lr"), (*self._bound, [self._lr])):
             spans += [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), kind, i)
                       for i, t in enumerate(ts) if t is not None and t.numel()]
         end, written_end = (0, None, None), (0, None, None)
         for a, b, kind, i in sorted(spans):
-            hit = end if kind != "grads" else written_end
+            written = kind in ("params", "masters")
+            hit = end if written else written_end
             if a < hit[0]:
                 raise ValueError(f"AdamW: {kind}[{i}] shares memory with {hit[1]}[{hit[2]}]")
             end = max(end, (b, kind, i), key=lambda e: e[0])
-            if kind != "grads":
+            if written:
                 written_end = max(written_end, (b, kind, i), key=lambda e: e[0])
 
     def step(self):

@@ -413,3 +413,15 @@ def test_the_reported_norm_decides(bits, scale, applied):
     assert (opt.steps, opt.skipped) == ((1, 0) if applied else (0, 1))
     same = [torch.equal(a, b) for a, b in zip(before, (*params, *masters, opt.m, opt.v))]
     assert not any(same[2:4]) if applied else all(same)
+
+
+def test_a_rate_in_written_memory_is_refused():
+    """The learning rate is read while parameters and masters are written; a gradient may hold it."""
+    w, g = torch.zeros(16, device="cuda"), torch.zeros(16, device="cuda")
+    p = torch.zeros(16, dtype=BF16, device="cuda")
+    for args in (([w], [g], None), ([p], [g], [w])):
+        with pytest.raises(ValueError, match="shares memory"):
+            optim.AdamW(*args, lr=w[3:4])
+    for lr in (g[3:4], torch.full((), 1e-3, device="cuda")):
+        optim.AdamW([w], [g], lr=lr).step()
+    torch.cuda.synchronize()
