@@ -76,7 +76,7 @@ class AdamW:
                                                g.dtype is torch.float32)
             self.offsets.append(at)
             at += -(-p.numel() // _BLOCK) * _BLOCK
-        self._lr = lr if isinstance(lr, torch.Tensor) else None
+        self._lr = lr.detach() if isinstance(lr, torch.Tensor) else None
         if self._lr is not None:
             if self._lr.numel() != 1:
                 raise ValueError("lr: expected one element")

@@ -425,3 +425,15 @@ def test_a_rate_in_written_memory_is_refused():
     for lr in (g[3:4], torch.full((), 1e-3, device="cuda")):
         optim.AdamW([w], [g], lr=lr).step()
     torch.cuda.synchronize()
+
+
+def test_the_bound_rate_stays():
+    """As with the tensors of the lists: what the caller does to its rate does not free what is bound."""
+    rate = torch.full((1,), 1e-3, device="cuda")
+    opt = optim.AdamW([torch.zeros(8, device="cuda")], [torch.ones(8, device="cuda")], lr=rate)
+    bound = rate.data_ptr()
+    rate.data = torch.zeros(1, device="cuda")
+    assert opt.lr.data_ptr() == bound == opt._config.lr_device and opt.lr.item() == rate.new_tensor(1e-3).item()
+    opt.lr = 2e-3
+    opt.step()
+    assert torch.all((opt._bound[0][0] + 2e-3).abs() < 1e-6)
