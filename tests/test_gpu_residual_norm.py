@@ -398,3 +398,60 @@ def test_branches_of_any_size(size, D):
         i["y"] *= size
     _check(6, D, change=change, eps=0.0, seed=D)
     _check(6, D, R=F32, W=F32, gate="token", change=change, eps=0.0, seed=D)
+
+
+# Wide rows by one CTA of 1024 threads (whole granules) and by a pair of CTAs, without sums of columns;
+# a whole gate of an fp32 residual is read from global memory there.
+@pytest.mark.parametrize("D", [8186, 8200, 12243, 16376, 16384])
+@pytest.mark.parametrize("R,W,G", [(BF16, BF16, BF16), (F32, F32, F32), (F32, BF16, BF16),
+                                   (BF16, F32, F32)])
+@pytest.mark.parametrize("post,gate,pre", [(True, "channel", True), (True, "full", True),
+                                           (False, "full", True), (False, "token", True),
+                                           (True, "none", False), (True, "token", True),
+                                           (False, "none", True), (True, "full", False)])
+def test_wide_rows_without_column_sums(D, R, W, G, post, gate, pre):
+    # More rows than two rounds of every SM have their weights staged, where those fit.
+    staged = D == 8200 and R is BF16 and gate in ("none", "token")
+    for M in (4, 301) if staged else (4,):
+        i = _inputs(M, D, R, W, post, gate, pre, D, G)
+        h, _, r_pre, r_post = block.residual_norm_forward(
+            i["h"], i["y"], i["w_pre"], i["w_post"], i["gate"], res_scale=0.5, branch_scale=1.25,
+            weight_offset=1.0)
+        got = dict(zip(("dh", "dy", "dw_pre", "dw_post", "dgate"), block.residual_norm_backward(
+            i["dn"], i["dh"], h, i["y"], r_pre, r_post, i["w_pre"], i["w_post"], i["gate"],
+            res_scale=0.5, branch_scale=1.25, weight_offset=1.0, need_dw=False,
+            need_dgate=gate in ("token", "full"))))
+        ref = oracle.backward(_np(i["dn"]), _np(i["dh"]), _np(h), _np(i["y"]), _np(r_pre),
+                              _np(r_post), _np(i["w_pre"]), _np(i["w_post"]), _np(i["gate"]), 0.5,
+                              1.25, 1.0)
+        assert got["dw_pre"] is got["dw_post"] is None
+        assert (got["dgate"] is not None) == (gate in ("token", "full"))
+        for name, t in got.items():
+            if t is None:
+                continue
+            want, mag = ref[name]
+            if name == "dgate" and gate == "token":
+                want, mag = want.sum(1, keepdims=True), mag.sum(1, keepdims=True)
+            assert t.shape == want.shape, name
+            _close(t, want, mag, 256, name)
+
+
+@pytest.mark.parametrize("D", [136, 35, 2056, 8192, 8200, 8191])
+def test_each_gradient_by_itself(D):
+    """What is not asked for changes nothing of what is."""
+    for gate in ("channel", "token", "full"):
+        i, (h, _, r_pre, r_post), whole = _check(7, D, gate=gate, seed=D)
+        f = lambda **kw: block.residual_norm_backward(  # noqa: E731
+            i["dn"], i["dh"], h, i["y"], r_pre, r_post, i["w_pre"], i["w_post"], i["gate"],
+            res_scale=0.5, branch_scale=1.25, weight_offset=1.0, **kw)
+        names = ("dh", "dy", "dw_pre", "dw_post", "dgate")
+        for kw in (dict(need_dw=False), dict(need_dgate=False), dict(need_dw=False, need_dgate=False)):
+            for name, t in zip(names, f(**kw)):
+                asked = kw.get("need_dgate", True) if name == "dgate" else \
+                    kw.get("need_dw", True) or not name.startswith("dw")
+                assert (t is not None) == asked, (name, kw)
+                if t is not None:
+                    # The sums of wide rows are split otherwise without columns to add up.
+                    same = torch.equal(t, whole[name])
+                    assert same or (D > 8185 and torch.allclose(t.float(), whole[name].float(),
+                                                                rtol=2 ** -7, atol=1e-3)), (name, kw)
