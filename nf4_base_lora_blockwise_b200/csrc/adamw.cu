@@ -21,9 +21,10 @@
 // 8 consecutive elements a lane, so every access is 16 or 32 bytes a lane (8 for codes) and a block's
 // scale is one warp reduction.  Codes are decoded through tables in shared memory; codes below the
 // grid's least value are rare and made by a second pass over the warp's block.
-// Measured: 42 M fp32 elements and moments, no norm (28 bytes an element) 233 us, 6.5 TB/s; 42 M bf16
-// ones in 448 tensors with masters, 8-bit moments and the clip, and the moments read as bf16 after
-// it, 220 us; 1.3 M in 14 tensors, 32 bits and the clip, 13.9 us.
+// Measured: 54.5 M fp32 elements and moments, no norm (28 bytes an element) 232 us, 6.6 TB/s; 42 M bf16
+// ones in 448 tensors with masters, 8-bit moments and the clip 180 us, with the moments read as bf16
+// after it 220; 1.3 M in 14 tensors, 32 bits and the clip, 13.9 us.  42 M bf16 without masters, 32 bits
+// and the clip: 235 us.
 #include <cuda_bf16.h>
 
 #include <cstdint>
@@ -40,7 +41,8 @@ namespace {
 constexpr int kAdamThreads = 256;
 constexpr int kAdamWarps = kAdamThreads / 32;
 
-// A 32-bit integer hash: multiplications by odd numbers between shifted exclusive ors.
+// A 32-bit integer hash, multiplications by odd numbers between shifted exclusive ors, with the shifts
+// and the two factors of C. Wellons, "Prospecting for Hash Functions" (2018).
 __device__ __forceinline__ uint32_t mix32(uint32_t x) {
   x = (x ^ (x >> 16)) * 0x7FEB352Du;
   x = (x ^ (x >> 15)) * 0x846CA68Bu;
@@ -547,7 +549,7 @@ int adam_ctas(uint32_t blocks, int cap) {
   return static_cast<int>(want < 1 ? 1 : (want < cap ? want : cap));
 }
 // CTAs of the step that the SMs hold at a time.  Three an SM with 80 registers, not four with 64 that
-// spill: 233 us against 247 (42 M elements, 32 bits) and 221 against 225 (8 bits, with norm and the moments read).
+// spill: 233 us against 247 (54.5 M elements, 32 bits) and 221 against 225 (8 bits, with norm and the moments read).
 // They draw chunks of blocks as they finish: with equal shares the SMs ended up to 15 % apart, 284 us.
 // A warp's two blocks a chunk: 221 us, with one 232, with four 235.
 constexpr int kStepCtas = 148 * 3, kRoundBits = 1;

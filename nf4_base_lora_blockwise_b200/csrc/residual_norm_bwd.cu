@@ -6,9 +6,9 @@
 //   dw_pre += (dn h) r_h,   S += (G y) (r_y k g),   a token's dgate = br r_y p,
 // v without the gate for a whole gate g, whose dgate is (G y) v br r_y.
 //
-// Bound by memory without the branch's norm: 16384 x 8192 bf16, weights frozen, 213 us, 6.3 TB/s.
+// Bound by memory without the branch's norm: 16384 x 8192 bf16, weights frozen, 201 us, 6.7 TB/s.
 // With it the two sums that every row waits for, and 16 warps an SM (128 registers a thread), bound
-// it: 4096 x 4096 with all gradients 44.5 us, 4.5 TB/s, some 5 of them for the sums of columns.
+// it: 4096 x 4096 with all gradients 44.3 us, 4.5 TB/s, some 5 of them for the sums of columns.
 // (1 / rms read with the row instead of a round ahead: 60 us.)
 #include "residual_norm.cuh"
 

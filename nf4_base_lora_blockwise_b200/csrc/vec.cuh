@@ -112,18 +112,6 @@ __device__ __forceinline__ float load_either1(const void* base, bool f32, int64_
              : __bfloat162float(static_cast<const __nv_bfloat16*>(base)[i]);
 }
 
-// What a value becomes when stored as T.
-template <typename T>
-__device__ __forceinline__ float stored(float x);
-template <>
-__device__ __forceinline__ float stored<float>(float x) {
-  return x;
-}
-template <>
-__device__ __forceinline__ float stored<__nv_bfloat16>(float x) {
-  return __bfloat162float(__float2bfloat16_rn(x));
-}
-
 // Two fp32 values in one register pair, with the rounding of the scalar operations.
 using f2 = unsigned long long;
 __device__ __forceinline__ f2 pair(float a, float b) {

@@ -13,6 +13,7 @@ BLOCK = 256
 
 
 def hash32(x):
+    """The 32-bit mixer whose constants C. Wellons, "Prospecting for Hash Functions" (2018), gives."""
     x = np.asarray(x, dtype=np.uint64) & 0xFFFFFFFF
     x = ((x ^ (x >> np.uint64(16))) * np.uint64(0x7FEB352D)) & np.uint64(0xFFFFFFFF)
     x = ((x ^ (x >> np.uint64(15))) * np.uint64(0x846CA68B)) & np.uint64(0xFFFFFFFF)
