@@ -23,11 +23,12 @@ class AdamW:
     them).  Both are bound at construction: the memory they have then is what every step reads
     and writes (a step can so be captured into a CUDA graph, and each replay takes the next one).
     masters: fp32 copies of the parameters that the step is taken on, None entries (or no list)
-    where there are none; a bf16 parameter without one is rounded stochastically.
+    where there are none; a bf16 parameter without one is rounded stochastically.  All of them start
+    at multiples of 16 bytes (step raises QLoraError otherwise, and for numbers out of range).
 
-    bits: 32 or 8 for the moments.  lr: a float, or a CUDA fp32 tensor of one element that is read
-    at every step.  lr_scales, weight_decays: one value a tensor (default 1 and weight_decay).
-    max_grad_norm: clips the norm over all gradients (None: not); grad_scale multiplies them first.
+    bits: 32 or 8 for the moments.  lr: a float, which a captured step keeps, or a CUDA fp32 tensor of
+    one element that is read at every step.  lr_scales, weight_decays: one value a tensor (default 1 and weight_decay).
+    max_grad_norm: clips the norm over all gradients (None or 0: not); grad_scale multiplies them first.
     check_finite: computes the norm without a clip too.  Where the norm is computed and is not
     finite (as the fp32 number that step() returns) the step changes nothing but that and
     ``skipped``.  seed: of the stochastic
