@@ -27,12 +27,12 @@ class AdamW:
     at multiples of 16 bytes (step raises QLoraError otherwise, and for numbers out of range).
 
     bits: 32 or 8 for the moments.  lr: a float, which a captured step keeps, or a CUDA fp32 tensor of
-    one element that is read at every step.  lr_scales, weight_decays: one value a tensor (default 1 and weight_decay).
-    max_grad_norm: clips the norm over all gradients (None or 0: not); grad_scale multiplies them first.
-    check_finite: computes the norm without a clip too.  Where the norm is computed and is not
-    finite (as the fp32 number that step() returns) the step changes nothing but that and
-    ``skipped``.  seed: of the stochastic
-    rounding, which is reproducible.  step: steps taken before.
+    one element that is read at every step.  lr_scales, weight_decays: one value a tensor (default
+    1 and weight_decay).  max_grad_norm: clips the norm over all gradients (None or 0: not);
+    grad_scale multiplies them first.  check_finite: computes the norm without a clip too.  Where
+    the norm is computed and is not finite (as the fp32 number that step() returns) the step
+    changes nothing but that and ``skipped``.  seed: of the stochastic rounding, which is
+    reproducible.  step: steps taken before.
 
     State: m, v: flat over the list, tensor i from offsets[i] on (every tensor starts a block of
     256 elements): fp32, or uint8 codes with the blocks' fp32 m_scale, v_scale.  It is zeroed on the
